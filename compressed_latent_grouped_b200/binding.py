@@ -11,13 +11,15 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from ctypes import POINTER, c_char_p, c_double, c_int, c_int32, c_size_t, c_uint64, c_void_p
+from ctypes import (POINTER, c_char_p, c_double, c_int, c_int32, c_int64, c_size_t, c_uint64,
+                    c_void_p)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libccgqa.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "ccgqa.h")
 
 F32, BF16 = 0, 1
+CACHE_I8, CACHE_E4M3 = 1, 2
 DEVERR_INDEX, DEVERR_TIMEOUT, DEVERR_CAPACITY = 1, 2, 4
 STATUS = {0: "OK", 1: "ERR_INVALID_ARG", 2: "ERR_UNSUPPORTED", 3: "ERR_CAPACITY",
           4: "ERR_WORKSPACE", 5: "ERR_CUDA"}
@@ -45,6 +47,21 @@ class ccgqa_kvcache(ctypes.Structure):
                 ("conv_hist_k", c_void_p), ("v_prev", c_void_p), ("batch", c_int32),
                 ("cap", c_int32), ("block_table", c_void_p), ("page_size", c_int32),
                 ("n_pages", c_int32)]
+
+
+class ccgqa_rows(ctypes.Structure):
+    _fields_ = [("ptr", c_void_p), ("batch", c_int64), ("token", c_int64), ("head", c_int64)]
+
+
+class ccgqa_cache8(ctypes.Structure):
+    _fields_ = [("format", c_int32), ("block", c_int32), ("k_scale", c_void_p),
+                ("v_scale", c_void_p)]
+
+
+class ccgqa_append(ctypes.Structure):
+    _fields_ = [("q", ccgqa_rows), ("q_out", ccgqa_rows), ("k", ccgqa_rows), ("v", ccgqa_rows),
+                ("k_out", ccgqa_rows), ("n_new", c_int32), ("n_valid", c_void_p),
+                ("pos", c_void_p)]
 
 
 class CCGQAError(RuntimeError):
@@ -98,6 +115,12 @@ def load() -> ctypes.CDLL:
                                            c_int32, c_void_p, c_void_p, P(ccgqa_weight_grads),
                                            c_void_p, c_size_t, c_void_p, c_void_p]
     lib.ccgqa_prefill_backward.restype = c_int
+    lib.ccgqa_kvcache_append_rope.argtypes = [P(ccgqa_config), P(ccgqa_kvcache), P(ccgqa_cache8),
+                                              P(ccgqa_append), c_void_p, c_void_p]
+    lib.ccgqa_kvcache_append_rope.restype = c_int
+    lib.ccgqa_kvcache_read.argtypes = [P(ccgqa_config), P(ccgqa_kvcache), P(ccgqa_cache8), c_int32,
+                                       c_int32, P(ccgqa_rows), P(ccgqa_rows), c_void_p, c_void_p]
+    lib.ccgqa_kvcache_read.restype = c_int
     lib.ccgqa_status_string.argtypes = [c_int]
     lib.ccgqa_status_string.restype = c_char_p
     lib.ccgqa_launch_count.argtypes = []
@@ -271,6 +294,42 @@ def ccgqa_prefill_backward(cfg, weights, x, batch, seq_len, dout, dx, grads, wor
                                     _ptr(dev_err), _stream(stream))
     if check and st != 0:
         raise CCGQAError(st, "ccgqa_prefill_backward")
+    return st
+
+
+def make_rows(t, order="bthd") -> ccgqa_rows:
+    """Head rows of a 4-D tensor whose dimensions are batch, token, head and
+    channel in `order` (channels last); None: absent."""
+    if t is None:
+        return ccgqa_rows(None, 0, 0, 0)
+    st = t.stride()
+    return ccgqa_rows(t.data_ptr(), *(st[order.index(c)] for c in "bth"))
+
+
+def make_cache8(fmt: int, block: int, k_scale, v_scale) -> ccgqa_cache8:
+    return ccgqa_cache8(fmt, block, k_scale.data_ptr(), v_scale.data_ptr())
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def ccgqa_kvcache_append_rope(cfg, cache, cache8, append: ccgqa_append, dev_err=None, stream=None,
+                              check=True) -> int:
+    st = load().ccgqa_kvcache_append_rope(ctypes.byref(cfg), ctypes.byref(cache), _ref(cache8),
+                                          ctypes.byref(append), _ptr(dev_err), _stream(stream))
+    if check and st != 0:
+        raise CCGQAError(st, "ccgqa_kvcache_append_rope")
+    return st
+
+
+def ccgqa_kvcache_read(cfg, cache, cache8, first, n, k_out: ccgqa_rows, v_out: ccgqa_rows,
+                       dev_err=None, stream=None, check=True) -> int:
+    st = load().ccgqa_kvcache_read(ctypes.byref(cfg), ctypes.byref(cache), _ref(cache8), first, n,
+                                   ctypes.byref(k_out), ctypes.byref(v_out), _ptr(dev_err),
+                                   _stream(stream))
+    if check and st != 0:
+        raise CCGQAError(st, "ccgqa_kvcache_read")
     return st
 
 

@@ -10,7 +10,7 @@
 #include <new>
 #include <utility>
 
-#include "kernels.h"
+#include "api_internal.h"
 
 namespace ccgqa {
 
@@ -66,7 +66,7 @@ int sm_count() {
 
 // Last CUDA error met by an entry point on this thread.
 static thread_local char t_last_error[256] = "no error";
-static ccgqa_status cuda_fail(cudaError_t e) {
+ccgqa_status cuda_fail(cudaError_t e) {
   snprintf(t_last_error, sizeof(t_last_error), "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
   return CCGQA_ERR_CUDA;
 }
@@ -82,18 +82,6 @@ static void phase_mark(int i, cudaStream_t st) {
     cudaEventRecord(static_cast<cudaEvent_t>(t_phase_events[i]), st);
 }
 
-namespace {
-
-struct Geo {
-  int E, C, Hq, Hkv, d, G, N, K;
-  int qk_mean, value_shift, causal, rope_on, channel_conv;
-  double rope_log2_base;
-  int dtype;
-  size_t es;  // element size
-};
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 // theta_i / (2 pi) * 2^64 with theta_i = base^(-2i/d) (RoPE, "Compressed
 // Convolutional Attention", Methodologie item 4), rounded to an integer in
 // extended precision; below 2^62 since theta_i <= 1.
@@ -102,7 +90,6 @@ uint64_t rope_turn_fraction(double log2_base, int i, int d) {
   const long double two_pi = 6.283185307179586476925286766559005768L;
   return static_cast<uint64_t>(llroundl(th / two_pi * 18446744073709551616.0L));
 }
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 ccgqa_status derive(const ccgqa_config* cfg, Geo* g) {
   if (!cfg) return CCGQA_ERR_INVALID_ARG;
@@ -139,7 +126,7 @@ ccgqa_status derive(const ccgqa_config* cfg, Geo* g) {
   return CCGQA_OK;
 }
 
-ccgqa_status check_weights(const Geo& g, const ccgqa_weights* w) {
+static ccgqa_status check_weights(const Geo& g, const ccgqa_weights* w) {
   if (!w) return CCGQA_ERR_INVALID_ARG;
   if (w->W_qkv && !aligned16(w->W_qkv)) return CCGQA_ERR_INVALID_ARG;
   if (g.K > 0 && g.channel_conv) {
@@ -189,6 +176,8 @@ PageMap page_map(const ccgqa_kvcache* c) {
   }
   return pm;
 }
+
+namespace {
 
 struct PrefillWs {
   size_t proj, q, k, v, total;

@@ -220,6 +220,51 @@ struct BwdArgs {
 template <typename T>
 cudaError_t launch_backward(const BwdArgs<T>& a, cudaStream_t stream);
 
+// ----------------------------------------------------------------- rows, 8-bit cache
+// Head rows [batch, tokens, heads, d] with strides in elements (ccgqa_rows).
+struct Rows {
+  void* ptr;
+  int64_t batch, token, head;
+};
+// Cache element formats (0: the working type), as ccgqa_cache_format.
+constexpr int kCacheI8 = 1, kCacheE4M3 = 2;
+
+// Append with the rotation (ccgqa_kvcache_append_rope).
+template <typename T>
+struct AppendArgs {
+  void *ck, *cv;             // T, or one byte per element
+  float *k_scale, *v_scale;  // 8-bit caches: one per block of 2^block_shift tokens and head
+  int block_shift;
+  PageMap pages;
+  int32_t* len;
+  int64_t cap;
+  int B, Hq, Hkv, d, n_new;
+  Rows q, q_out, k, v, k_out;   // q, q_out, k_out may be absent (ptr null)
+  const int32_t *n_valid, *pos;
+  int rope_on;
+  uint64_t rope_frac[64];       // as in PreAttnArgs
+  int32_t* dev_err;
+  // set by the launcher
+  int tile_tokens, bump_here;
+};
+template <typename T>
+cudaError_t launch_append_rope(const AppendArgs<T>& a, int fmt, cudaStream_t stream);
+
+// Cached rows [first, first + n) back as values of T (ccgqa_kvcache_read).
+struct ReadArgs {
+  const void *ck, *cv;
+  const float *k_scale, *v_scale;
+  int block_shift;
+  PageMap pages;
+  const int32_t* len;
+  int64_t cap;
+  int B, Hkv, d, first, n;
+  Rows k_out, v_out;
+  int32_t* dev_err;
+};
+template <typename T>
+cudaError_t launch_kv_read(const ReadArgs& a, int fmt, cudaStream_t stream);
+
 // Split plan for the decode step, shared by the workspace-size query and the launch.
 void decode_plan(int B, int Hkv, int E, int N, int64_t cap, bool has_proj, int es,
                  int* e_splits, int* splits, int* chunk);

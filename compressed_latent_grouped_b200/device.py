@@ -149,6 +149,170 @@ class DeviceLayer:
         return int(self.dev_err.item())
 
 
+def _bad(where: str, what: str):
+    raise B.CCGQAError(1, f"{where}: {what}")
+
+
+def _check(where, name, t, shape, dtype, device, optional=False):
+    """Shape, type, device and channel stride of a tensor argument."""
+    if t is None:
+        if optional:
+            return
+        _bad(where, f"{name} is missing")
+    if tuple(t.shape) != tuple(shape):
+        _bad(where, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        _bad(where, f"{name} is {t.dtype}, expected {dtype}")
+    if t.device != device:
+        _bad(where, f"{name} is on {t.device}, expected {device}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        _bad(where, f"the last dimension of {name} is not contiguous")
+
+
+def _check_dense(where, name, t, shape, dtype, device, optional=False):
+    _check(where, name, t, shape, dtype, device, optional)
+    if t is not None and not t.is_contiguous():
+        _bad(where, f"{name} is not contiguous")
+
+
+def head_dim(cfg: B.ccgqa_config) -> int:
+    return cfg.E // (cfg.C * cfg.n_q_heads)
+
+
+def _dtype_of(cfg: B.ccgqa_config):
+    return torch.float32 if cfg.dtype == B.F32 else torch.bfloat16
+
+
+class DeviceKVCache:
+    """A KV cache for finished query / key / value rows, without a layer's
+    weights: contiguous [batch, Hkv, cap, d] or paged (a pool [n_pages, Hkv,
+    page_size, d] and a block table [batch, cap / page_size]), in the
+    configuration's type or in 8 bits with one fp32 scale per ``block`` tokens
+    and kv head.
+
+    The handle keeps pointers, so the tensors must stay where they are; it
+    keeps nothing of their contents.  Calls run on ``stream`` (default: the
+    current stream of the cache's device)."""
+
+    FORMATS = {"i8": (B.CACHE_I8, torch.int8), "e4m3": (B.CACHE_E4M3, torch.float8_e4m3fn)}
+
+    def __init__(self, cfg, batch: int, cap: int, fmt: str = "native", block: int = 64,
+                 block_table: torch.Tensor | None = None, page_size: int = 0, n_pages: int = 0,
+                 device="cuda"):
+        """Allocate an empty cache: ``fmt`` is "native", "i8" or "e4m3"."""
+        if fmt != "native" and fmt not in self.FORMATS:
+            _bad("DeviceKVCache", f"unknown format {fmt!r}")
+        if block_table is not None and page_size < 1:
+            _bad("DeviceKVCache", "a paged cache needs its page size")
+        if fmt != "native" and (block < 1 or cap % block or (block_table is not None and
+                                                             page_size % block)):
+            _bad("DeviceKVCache", f"blocks of {block} tokens do not divide the cache")
+        dev = torch.device(device)
+        H, d = cfg.n_kv_heads, head_dim(cfg)
+        lead, rows = ((batch, H), cap) if block_table is None else ((n_pages, H), page_size)
+        dt = _dtype_of(cfg) if fmt == "native" else self.FORMATS[fmt][1]
+        kv = [torch.zeros(*lead, rows, d, dtype=torch.uint8 if fmt == "e4m3" else dt, device=dev).view(dt)
+              for _ in range(2)]
+        sc = [None, None] if fmt == "native" else [
+            torch.zeros(*lead, rows // block, dtype=torch.float32, device=dev) for _ in range(2)]
+        self._bind(cfg, kv[0], kv[1], torch.zeros(batch, dtype=torch.int32, device=dev), sc[0], sc[1],
+                   block_table)
+
+    @classmethod
+    def wrap(cls, cfg, k, v, len_, k_scale=None, v_scale=None, block_table=None):
+        """A handle on tensors the caller owns; the type of ``k`` (the
+        configuration's, int8 or float8_e4m3fn) says the format, and the shape
+        of the scales the block."""
+        self = cls.__new__(cls)
+        self._bind(cfg, k, v, len_, k_scale, v_scale, block_table)
+        return self
+
+    def _bind(self, cfg, k, v, len_, k_scale, v_scale, block_table):
+        where = "DeviceKVCache"
+        self.cfg, self.device, self.d = cfg, k.device, head_dim(cfg)
+        if self.device.type != "cuda":
+            raise RuntimeError("CCGQA needs a CUDA device")
+        self.dtype = _dtype_of(cfg)
+        fmt = {torch.int8: B.CACHE_I8, torch.float8_e4m3fn: B.CACHE_E4M3}.get(k.dtype, 0)
+        if k.dim() != 4:
+            _bad(where, "k is not 4-dimensional")
+        shape = (k.shape[0], cfg.n_kv_heads, k.shape[2], self.d)
+        dt = k.dtype if fmt else self.dtype
+        _check_dense(where, "k", k, shape, dt, self.device)
+        _check_dense(where, "v", v, shape, dt, self.device)
+        if block_table is not None:
+            if block_table.dim() != 2:
+                _bad(where, "block_table is not 2-dimensional")
+            block_table = block_table.to(self.device, torch.int32).contiguous()
+        self.batch = k.shape[0] if block_table is None else block_table.shape[0]
+        self.cap = k.shape[2] if block_table is None else block_table.shape[1] * k.shape[2]
+        _check_dense(where, "len", len_, (self.batch,), torch.int32, self.device)
+        self.block, self.cache8 = 0, None
+        if fmt:
+            if k_scale is None or k_scale.dim() != 3 or not k_scale.shape[2] or k.shape[2] % k_scale.shape[2]:
+                _bad(where, "an 8-bit cache needs scales [..., Hkv, tokens / block]")
+            self.block = k.shape[2] // k_scale.shape[2]
+            sshape = (*shape[:2], shape[2] // self.block)
+            _check_dense(where, "k_scale", k_scale, sshape, torch.float32, self.device)
+            _check_dense(where, "v_scale", v_scale, sshape, torch.float32, self.device)
+            self.cache8 = B.make_cache8(fmt, self.block, k_scale, v_scale)
+        elif k_scale is not None or v_scale is not None:
+            _bad(where, "scales go with an 8-bit cache")
+        self.k, self.v, self.len, self.k_scale, self.v_scale = k, v, len_, k_scale, v_scale
+        self.block_table = block_table
+        self.cache = B.make_kvcache(k, v, len_, block_table=block_table)
+        self.dev_err = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def append_rope(self, k, v, q=None, q_out=None, k_out=None, n_valid=None, pos=None, stream=None):
+        """Append rows k, v [batch, n, Hkv, d], keys rotated; with q [batch, n,
+        Hq, d] also returns the rotated queries (``q_out``, allocated if not
+        given).  ``n_valid`` [batch] int32: rows that count per sequence;
+        ``pos`` [batch] int32: position of the first row (default: len)."""
+        where, dev, dt, d = "append_rope", self.device, self.dtype, self.d
+        if k.dim() != 4:
+            _bad(where, "k is not 4-dimensional")
+        n = k.shape[1]
+        kv = (self.batch, n, self.cfg.n_kv_heads, d)
+        qs = (self.batch, n, self.cfg.n_q_heads, d)
+        _check(where, "k", k, kv, dt, dev)
+        _check(where, "v", v, kv, dt, dev)
+        _check(where, "k_out", k_out, kv, dt, dev, True)
+        if q is None and q_out is not None:
+            _bad(where, "q_out without q")
+        _check(where, "q", q, qs, dt, dev, True)
+        _check_dense(where, "n_valid", n_valid, (self.batch,), torch.int32, dev, True)
+        _check_dense(where, "pos", pos, (self.batch,), torch.int32, dev, True)
+        with torch.cuda.device(dev):
+            if q is not None and q_out is None:
+                q_out = torch.empty(qs, dtype=dt, device=dev)
+            _check(where, "q_out", q_out, qs, dt, dev, q is None)
+            ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+            a = B.ccgqa_append(B.make_rows(q), B.make_rows(q_out), B.make_rows(k), B.make_rows(v),
+                               B.make_rows(k_out), n, ptr(n_valid), ptr(pos))
+            B.ccgqa_kvcache_append_rope(self.cfg, self.cache, self.cache8, a, self.dev_err, stream)
+        return q_out
+
+    def read(self, first: int, n: int, k_out=None, v_out=None, stream=None):
+        """Tokens [first, first + n) of every sequence as values, (k, v)
+        [batch, Hkv, n, d]; rows past a sequence's length keep what the output
+        held (zeros when allocated here)."""
+        shape = (self.batch, self.cfg.n_kv_heads, n, self.d)
+        with torch.cuda.device(self.device):
+            if k_out is None:
+                k_out = torch.zeros(shape, dtype=self.dtype, device=self.device)
+            if v_out is None:
+                v_out = torch.zeros(shape, dtype=self.dtype, device=self.device)
+            _check("read", "k_out", k_out, shape, self.dtype, self.device)
+            _check("read", "v_out", v_out, shape, self.dtype, self.device)
+            B.ccgqa_kvcache_read(self.cfg, self.cache, self.cache8, first, n,
+                                 B.make_rows(k_out, "bhtd"), B.make_rows(v_out, "bhtd"), self.dev_err,
+                                 stream)
+        return k_out, v_out
+
+    def error_bits(self) -> int:
+        return int(self.dev_err.item())
+
+
 class Graph:
     """Library calls recorded once into a CUDA graph (ccgqa_graph_*) and
     launched again with the same arguments: ``Graph(fn, stream)`` records what

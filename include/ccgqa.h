@@ -309,6 +309,88 @@ CCGQA_API ccgqa_status ccgqa_output_projection(const ccgqa_config* cfg, const vo
                                                const void* o, int64_t M, void* y,
                                                int32_t* dev_err, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Cache operators on rows that are already queries, keys and values (a plain
+ * grouped-query layer, or one that makes its own rows).
+ * Of cfg they use E, C, n_q_heads, n_kv_heads (head dim d = E / (C Hq)), dtype
+ * and, where stated, rope_base; cfg is validated as for every call.
+ * ------------------------------------------------------------------------- */
+
+/* A tensor of head rows [batch, tokens, heads, d]: element (b, t, h, e) lies at
+ * ptr[b * batch + t * token + h * head + e] (strides in elements of cfg->dtype).
+ * The d elements of a row are contiguous; ptr and every stride in bytes are
+ * multiples of 16; the rows do not overlap (a stride of a dimension longer
+ * than one covers the dimensions with smaller strides, so no stride is zero or
+ * negative there).  Slices of a packed q | k | v projection, [B, S, H, d] and
+ * the cache's [B, H, S, d] order all fit.  Anything else: CCGQA_ERR_INVALID_ARG. */
+typedef struct {
+  void* ptr;
+  int64_t batch, token, head;
+} ccgqa_rows;
+
+/* An 8-bit cache: cache->k / cache->v of a ccgqa_kvcache hold one byte per
+ * element, in the same layouts, and each block of `block` consecutive tokens of
+ * a kv head has one fp32 scale for k and one for v: value = code * scale.
+ * Scales: [batch, Hkv, cap / block], or for a paged cache [n_pages, Hkv,
+ * page_size / block].  block is 16, 32, 64 or 128, divides cap, and does not
+ * exceed page_size.  Scale pointers are 4-byte aligned, device, caller-owned. */
+typedef enum { CCGQA_CACHE_I8 = 1, CCGQA_CACHE_E4M3 = 2 } ccgqa_cache_format;
+typedef struct {
+  int32_t format;   /* CCGQA_CACHE_I8: two's complement, codes -127..127;
+                       CCGQA_CACHE_E4M3: 4 exponent and 3 mantissa bits, largest 448 */
+  int32_t block;    /* tokens per scale */
+  float* k_scale;
+  float* v_scale;
+} ccgqa_cache8;
+
+/* Append k / v rows to the cache with the rotary position embedding (RoPE) of
+ * q and k on the way.  Row i < n_valid[b] of sequence b (n_valid NULL: i <
+ * n_new for all) becomes token len[b] + i; then len[b] += n_valid[b].
+ *  - Rotation as everywhere in this library: pairs (i, i + d/2), base
+ *    cfg->rope_base (0: none), position pos[b] + i (pos NULL: len[b] + i).
+ *    Products in fp32, the angle reduced exactly.  v is not rotated.
+ *  - q, q_out: [batch, n_new, Hq, d], both or neither; q_out receives the
+ *    rotated queries.  k, v: [batch, n_new, Hkv, d].  k_out (nullable, like k)
+ *    also receives the rotated keys in cfg->dtype.  q_out may be q and k_out
+ *    may be k (the same pointer and strides); other overlaps are the caller's
+ *    error.  Rows i >= n_valid[b] are neither read nor written.
+ *  - c8 NULL: k and v are stored in cfg->dtype.  Otherwise they are quantised:
+ *    for each touched block and kv head, amax = max |x| over the block's new
+ *    rows, scale = max(old scale, amax / 127 or / 448), where the old scale
+ *    counts only if the block holds earlier tokens of this sequence; if the
+ *    scale grew, those tokens' codes are rounded again to
+ *    rn(code * old / new); new codes are rn(x / scale), ties to even.  A block
+ *    with an infinity or NaN gets a non-finite scale, so all its values read
+ *    back as NaN or infinity until the block is begun anew.
+ *  - A sequence with len[b] + n_valid[b] > cap (or len[b] < 0) sets
+ *    CCGQA_DEVERR_CAPACITY and is left alone, its q_out and k_out rows too;
+ *    n_valid[b] outside [0, n_new] sets CCGQA_DEVERR_INDEX, likewise.  A page id
+ *    outside the pool sets CCGQA_DEVERR_INDEX and those tokens' rows are not
+ *    stored (len still grows).  Conv histories and v_prev are not touched.
+ * n_valid, pos: [batch] int32, device, nullable.  n_new > cap:
+ * CCGQA_ERR_CAPACITY; n_new == 0: nothing is done. */
+typedef struct {
+  ccgqa_rows q, q_out, k, v, k_out;   /* ptr NULL = absent (q, q_out, k_out) */
+  int32_t n_new;
+  const int32_t* n_valid;
+  const int32_t* pos;
+} ccgqa_append;
+CCGQA_API ccgqa_status ccgqa_kvcache_append_rope(const ccgqa_config* cfg,
+                                                 const ccgqa_kvcache* cache,
+                                                 const ccgqa_cache8* c8, const ccgqa_append* a,
+                                                 int32_t* dev_err, void* stream);
+
+/* Read tokens [first, first + n) of every sequence back as values in
+ * cfg->dtype (8-bit codes times their scale, rounded once): row i of k_out /
+ * v_out [batch, n, Hkv, d] is token first + i.  Rows of tokens at or past
+ * len[b] are left as they are.  0 <= first, n; first + n <= cap (else
+ * CCGQA_ERR_CAPACITY).  len[b] outside [0, cap] sets CCGQA_DEVERR_CAPACITY, a
+ * page id outside the pool CCGQA_DEVERR_INDEX; those rows are left as they are. */
+CCGQA_API ccgqa_status ccgqa_kvcache_read(const ccgqa_config* cfg, const ccgqa_kvcache* cache,
+                                          const ccgqa_cache8* c8, int32_t first, int32_t n,
+                                          const ccgqa_rows* k_out, const ccgqa_rows* v_out,
+                                          int32_t* dev_err, void* stream);
+
 /* Static description of a status code. */
 CCGQA_API const char* ccgqa_status_string(ccgqa_status s);
 

@@ -1,0 +1,270 @@
+"""ccgqa_kvcache_append_rope and ccgqa_kvcache_read against float64: caches in
+the working type and in 8 bits, contiguous and paged."""
+import numpy as np
+import pytest
+import torch
+
+from compressed_latent_grouped_b200 import binding as B
+from compressed_latent_grouped_b200.device import DeviceKVCache, Graph
+from rows_ref import (CODE_ERR, QMAX, assert_within, config, dense_rows, f64, half_step, rotate,
+                      rotate_slack, torch_dtype)
+
+pytestmark = pytest.mark.gpu
+
+
+def _table(rng, batch, per_seq, spare=3):
+    ids = rng.permutation(batch * per_seq + spare)[: batch * per_seq]
+    return torch.from_numpy(ids.astype(np.int32).reshape(batch, per_seq)).cuda(), batch * per_seq + spare
+
+
+def _cache(cfg, batch, cap, fmt, block, page, rng, lens):
+    """A cache full of random rows (what earlier sequences left), lengths set."""
+    table, pages = _table(rng, batch, cap // page) if page else (None, 0)
+    c = DeviceKVCache(cfg, batch, cap, fmt=fmt, block=block, block_table=table, page_size=page, n_pages=pages)
+    g = torch.Generator(device="cuda").manual_seed(int(rng.randint(1 << 30)))
+    for x, sc in ((c.k, c.k_scale), (c.v, c.v_scale)):
+        r = torch.randn(x.shape, generator=g, device="cuda")
+        if fmt == "native":
+            x.copy_(r)
+            continue
+        q = (r * 40).round().clamp(-127, 127) if fmt == "i8" else (r * 100).clamp(-448, 448)
+        x.view(torch.uint8).copy_(q.to(x.dtype).view(torch.uint8))
+        sc.copy_(torch.rand(sc.shape, generator=g, device="cuda") * 0.05 + 0.001)
+    c.len.copy_(torch.tensor(lens, dtype=torch.int32))
+    return c, table
+
+
+def _check_append(c, table, before, k, v, lens, n_valid, pos, base, dtype, fmt, block, what):
+    """The cache after an append against the definition, element by element."""
+    hs = half_step(dtype)
+    for name, new in (("k", k), ("v", v)):
+        x0, s0 = before[name]
+        x1 = dense_rows(getattr(c, name), table)
+        s1 = None if fmt == "native" else dense_rows(getattr(c, name + "_scale"), table)
+        for b in range(c.batch):
+            L, n = lens[b], n_valid[b]
+            raw = f64(new[b, :n])
+            rows = raw if name == "v" else rotate(raw, pos[b] + np.arange(n), base)
+            slack = np.zeros_like(rows) if name == "v" or base == 0.0 else rotate_slack(raw)
+            rows, slack = rows.transpose(1, 0, 2), slack.transpose(1, 0, 2)
+            if fmt == "native":
+                assert_within(x1[b, :, L:L + n], rows, np.abs(rows) * hs * (base != 0.0 and name == "k")
+                              + slack * (1 + hs), f"{what} {name}")
+                x1[b, :, L:L + n] = x0[b, :, L:L + n]
+                assert np.array_equal(x1[b], x0[b]), f"{what} {name}: rows outside the append changed"
+                continue
+            rel, absolute = CODE_ERR[fmt]
+            for j in range(x0.shape[2] // block):
+                lo, hi = max(L, j * block), min(L + n, (j + 1) * block)
+                blk = slice(j * block, (j + 1) * block)
+                if hi <= lo:
+                    assert np.array_equal(x1[b, :, blk], x0[b, :, blk]) and np.array_equal(s1[b, :, j], s0[b, :, j])
+                    continue
+                part, sl = rows[:, lo - L:hi - L], slack[:, lo - L:hi - L]
+                held = s0[b, :, j] if j * block < L else 0.0
+                s = np.maximum(held, np.abs(part).max((1, 2)) / QMAX[fmt])
+                # one fp32 division, and the rotation's error of the largest element
+                assert_within(s1[b, :, j], s, s * 2.0 ** -24 + sl.max((1, 2)) / QMAX[fmt], f"{what} {name} scale")
+                sj = s1[b, :, j][:, None, None]
+                # a code is off by half a step, and x / s by an fp32 rounding (of up to QMAX steps)
+                tol = np.abs(part) * rel + sj * (absolute + QMAX[fmt] * 2.0 ** -22) + sl
+                assert_within(x1[b, :, lo:hi] * sj, part, tol, f"{what} {name} codes")
+                old = x0[b, :, j * block:lo] * np.asarray(held).reshape(-1, 1, 1)
+                grew = (s1[b, :, j] > held).reshape(-1, 1, 1)
+                tol = np.where(grew, np.abs(old) * rel + sj * (absolute + QMAX[fmt] * 2.0 ** -22), 0.0)
+                assert_within(x1[b, :, j * block:lo] * sj, old, tol, f"{what} {name} held codes")
+                assert np.array_equal(x1[b, :, hi:(j + 1) * block], x0[b, :, hi:(j + 1) * block]), "rows past the end"
+
+
+CASES = [
+    # Hq, Hkv, d, dtype, fmt, block, cap, page, lens, n, n_valid, base
+    (8, 2, 64, "bf16", "native", 0, 128, 0, (5, 0, 127), 1, None, 1e4),
+    (8, 2, 64, "bf16", "native", 0, 128, 16, (5, 0, 127), 1, None, 5e5),
+    (16, 4, 32, "bf16", "native", 0, 256, 64, (63, 1), 77, (77, 0), 1e4),
+    (3, 3, 128, "f32", "native", 0, 96, 32, (31, 40), 19, (7, 19), 1e4),
+    (2, 1, 16, "f32", "native", 0, 64, 0, (0,), 64, None, 0.0),
+    (8, 2, 64, "bf16", "i8", 16, 128, 0, (5, 0, 127), 1, None, 1e4),
+    (8, 2, 64, "bf16", "i8", 64, 192, 64, (5, 64, 127), 65, (65, 0, 64), 5e5),
+    (16, 1, 32, "bf16", "e4m3", 32, 128, 32, (31, 32), 33, None, 1e4),
+    (4, 4, 128, "bf16", "e4m3", 128, 256, 128, (100,), 156, None, 1e4),
+    (6, 3, 32, "f32", "i8", 32, 96, 32, (17, 95), 1, None, 1e4),
+    (2, 2, 16, "f32", "e4m3", 16, 64, 16, (3, 15), 40, (40, 2), 0.0),
+    (40, 8, 128, "bf16", "i8", 64, 448, 64, (201,), 247, None, 5e5),
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,dtype,fmt,block,cap,page,lens,n,n_valid,base", CASES)
+def test_append_and_read(Hq, Hkv, d, dtype, fmt, block, cap, page, lens, n, n_valid, base):
+    rng = np.random.RandomState(n * 31 + d)
+    cfg = config(Hq, Hkv, d, dtype, base)
+    batch = len(lens)
+    c, table = _cache(cfg, batch, cap, fmt, block, page, rng, lens)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn(batch, n, Hq + 2 * Hkv, d, generator=g, device="cuda").to(torch_dtype(dtype))
+    q, k, v = x.split([Hq, Hkv, Hkv], 2)     # packed rows: strided heads
+    keep = x.clone()
+    nv = torch.tensor(n_valid, dtype=torch.int32).cuda() if n_valid else None
+    n_valid = n_valid or (n,) * batch
+    before = {m: (dense_rows(getattr(c, m), table),
+                  None if fmt == "native" else dense_rows(getattr(c, m + "_scale"), table)) for m in ("k", "v")}
+    q_out = torch.full((batch, n, Hq, d), 9.0, dtype=x.dtype, device="cuda")
+    k_out = torch.full((batch, n, Hkv, d), 9.0, dtype=x.dtype, device="cuda")
+    assert c.append_rope(k, v, q=q, q_out=q_out, k_out=k_out, n_valid=nv) is q_out
+    torch.cuda.synchronize()
+    assert c.error_bits() == 0
+    assert torch.equal(x, keep)
+    assert c.len.tolist() == [a + b for a, b in zip(lens, n_valid)]
+    hs = half_step(dtype)
+    for b in range(batch):
+        m = n_valid[b]
+        for got, src in ((q_out, q), (k_out, k)):
+            raw = f64(src[b, :m])
+            ref = rotate(raw, lens[b] + np.arange(m), base)
+            assert_within(f64(got[b, :m]), ref, np.abs(ref) * hs + rotate_slack(raw) * 2, "rotated rows")
+            assert (got[b, m:] == 9.0).all(), "rows that do not count were written"
+    _check_append(c, table, before, k, v, lens, n_valid, lens, base, dtype, fmt, block, "append")
+
+    # read back: values of the stored codes, rounded once; rows past the length stay
+    first = min(3, cap - 1)
+    ko = torch.full((batch, Hkv, cap - first, d), 5.0, dtype=x.dtype, device="cuda")
+    vo = ko.clone()
+    c.read(first, cap - first, ko, vo)
+    torch.cuda.synchronize()
+    for name, got in (("k", ko), ("v", vo)):
+        ref = dense_rows(getattr(c, name), table)
+        if fmt != "native":
+            ref = ref * np.repeat(dense_rows(getattr(c, name + "_scale"), table), block, 2)[..., None]
+        for b in range(batch):
+            end = lens[b] + n_valid[b]
+            r = ref[b, :, first:end]
+            # one fp32 product, then the rounding to the output's type
+            assert_within(f64(got[b, :, :max(end - first, 0)]), r,
+                          np.abs(r) * (0.0 if fmt == "native" else hs + 2.0 ** -23), f"read {name}")
+            assert (got[b, :, max(end - first, 0):] == 5.0).all()
+
+
+def test_tokens_one_by_one_equal_the_definition():
+    """Blocks that grow token by token: every held code stays within half a
+    step of each rescale that touched it."""
+    cfg = config(4, 2, 32, "bf16", 1e4)
+    c = DeviceKVCache(cfg, 2, 64, fmt="i8", block=16)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(2, 40, 2, 32, generator=g, device="cuda").bfloat16()
+    y = torch.randn(2, 40, 2, 32, generator=g, device="cuda").bfloat16()
+    for t in range(40):
+        c.append_rope(x[:, t:t + 1], y[:, t:t + 1])
+    torch.cuda.synchronize()
+    assert c.len.tolist() == [40, 40] and c.error_bits() == 0
+    for b in range(2):
+        ref = rotate(f64(x[b]), np.arange(40), 1e4)
+        for name, r in (("k", ref), ("v", f64(y[b]))):
+            s = np.repeat(f64(getattr(c, name + "_scale")[b]), 16, 1)[:, :40, None]
+            got = f64(getattr(c, name)[b])[:, :40] * s
+            # scales only grow, so each of at most 16 roundings is below half the final step
+            assert_within(got, r.transpose(1, 0, 2), 8.0 * s, name)
+            amax = np.abs(r.transpose(1, 0, 2)).reshape(2, 40 * 32)
+            assert np.all(s[:, 0, 0] >= amax[:, :16 * 32].max(1) / 127 * (1 - 2.0 ** -20))
+
+
+def test_positions_and_in_place():
+    cfg = config(4, 2, 64, "f32", 1e4)
+    c = DeviceKVCache(cfg, 2, 64)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q = torch.randn(2, 3, 4, 64, generator=g, device="cuda")
+    k = torch.randn(2, 3, 2, 64, generator=g, device="cuda")
+    v = torch.randn(2, 3, 2, 64, generator=g, device="cuda")
+    q0, k0 = q.clone(), k.clone()
+    pos = torch.tensor([2 ** 30 - 1, 12345], dtype=torch.int32).cuda()
+    c.append_rope(k, v, q=q, q_out=q, k_out=k, pos=pos)
+    torch.cuda.synchronize()
+    for b, p in enumerate(pos.tolist()):
+        for got, raw in ((q, q0), (k, k0)):
+            r = f64(raw[b])
+            theta = 1e4 ** (-2.0 * np.arange(32, dtype=np.longdouble) / 64)
+            # the fraction of a turn theta / 2 pi is held in 64 bits: off by 2^-65 p turns at most;
+            # the reference reduces the angle in extended precision
+            ang = (np.arange(p, p + 3, dtype=np.longdouble)[:, None, None] * theta) % (2 * np.longdouble(np.pi))
+            lo, hi = r[..., :32], r[..., 32:]
+            ref = np.concatenate([lo * np.cos(ang) - hi * np.sin(ang), lo * np.sin(ang) + hi * np.cos(ang)], -1)
+            # the reference's pi and powers carry 2^-52 relative: p 2^-52 rad of its own
+            slack = rotate_slack(r) + (np.abs(np.concatenate([lo, lo], -1)) + np.abs(np.concatenate([hi, hi], -1))) * p * 2.0 ** -51
+            assert_within(f64(got[b]), ref.astype(np.float64), np.abs(ref.astype(np.float64)) * 2.0 ** -24 + slack, "far positions")
+        assert np.array_equal(f64(c.k[b, :, :3]), f64(k[b]).transpose(1, 0, 2))
+
+
+@pytest.mark.parametrize("fmt", ["native", "i8", "e4m3"])
+def test_device_checks(fmt):
+    """Overfull sequences, bad counts and pages set error bits and leave the rest right."""
+    cfg = config(4, 2, 32, "bf16", 1e4)
+    rng = np.random.RandomState(1)
+    lens = [62, 10, -1, 5]
+    c, _ = _cache(cfg, 4, 64, fmt, 16, 0, rng, lens)
+    ref, _ = _cache(cfg, 4, 64, fmt, 16, 0, np.random.RandomState(1), lens)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    k = torch.randn(4, 3, 2, 32, generator=g, device="cuda").bfloat16()
+    q = torch.randn(4, 3, 4, 32, generator=g, device="cuda").bfloat16()
+    qo = torch.zeros_like(q)
+    c.append_rope(k, k, q=q, q_out=qo, n_valid=torch.tensor([3, 2, 1, 4], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert c.error_bits() == B.DEVERR_CAPACITY | B.DEVERR_INDEX
+    assert c.len.tolist() == [62, 12, -1, 5]
+    raw = lambda t: t.view(torch.uint8)  # noqa: E731
+    for b in (0, 2, 3):
+        assert torch.equal(raw(c.k[b]), raw(ref.k[b])) and torch.equal(raw(c.v[b]), raw(ref.v[b]))
+        assert not qo[b].any()
+    assert qo[1, :2].any() and not qo[1, 2].any()
+
+    # a page id outside the pool: the tokens of that page are dropped, the others stored
+    table = torch.tensor([[0, 99], [2, -5]], dtype=torch.int32).cuda()
+    p = DeviceKVCache(cfg, 2, 64, fmt=fmt, block=16, block_table=table, page_size=32, n_pages=4)
+    p.append_rope(torch.cat([k] * 14, 1)[:2, :40], torch.cat([k] * 14, 1)[:2, :40])
+    torch.cuda.synchronize()
+    assert p.error_bits() == B.DEVERR_INDEX and p.len.tolist() == [40, 40]
+    val = p.k.float()
+    assert val[0].any(-1).all() and val[2].any(-1).all() and not val[1].any() and not val[3].any()
+    p.dev_err.zero_()
+    ko, _ = p.read(0, 40)
+    torch.cuda.synchronize()
+    assert p.error_bits() == B.DEVERR_INDEX and ko[:, :, :32].any(-1).all() and not ko[:, :, 32:].any()
+
+
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+def test_zero_and_non_finite_blocks(fmt):
+    cfg = config(2, 2, 16, "bf16", 0.0)
+    c = DeviceKVCache(cfg, 1, 64, fmt=fmt, block=16)
+    k = torch.randn(1, 48, 2, 16, device="cuda").bfloat16()
+    v = k.clone()
+    k[:, :16] = 0
+    k[0, 20, 0, 3] = float("nan")
+    v[0, 40, 1, 2] = float("inf")
+    c.append_rope(k, v)
+    ko, vo = c.read(0, 48)
+    torch.cuda.synchronize()
+    assert not ko[0, :, :16].any() and (c.k_scale[0, :, 0] == 0).all()
+    assert not ko[0, 0, 16:32].isfinite().any() and ko[0, 1].isfinite().all()
+    assert not vo[0, 1, 32:48].isfinite().any() and vo[0, 0].isfinite().all()
+    c.len.zero_()                       # begun anew, the block is sound again
+    c.append_rope(v[:, :16], v[:, :16])
+    c.append_rope(v[:, :16], v[:, :16])
+    ko, _ = c.read(0, 32)
+    assert ko[:, :, :32].isfinite().all()
+
+
+def test_streams_graphs_and_empty_calls():
+    cfg = config(4, 2, 64, "bf16", 1e4)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k = torch.randn(2, 5, 2, 64, generator=g, device="cuda").bfloat16()
+    a = DeviceKVCache(cfg, 2, 64, fmt="i8", block=16)
+    b = DeviceKVCache(cfg, 2, 64, fmt="i8", block=16)
+    a.append_rope(k[:, :0], k[:, :0])
+    assert a.len.tolist() == [0, 0]
+    for _ in range(3):
+        a.append_rope(k, k)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    gr = Graph(lambda: b.append_rope(k, k), s)
+    for _ in range(3):
+        gr.launch()
+    torch.cuda.synchronize()
+    assert torch.equal(a.k, b.k) and torch.equal(a.v_scale, b.v_scale) and torch.equal(a.len, b.len)
+    gr.close()

@@ -1,0 +1,95 @@
+"""Host checks of the operators on finished rows (no GPU needed): nothing is
+launched on a bad argument."""
+import ctypes
+import os
+import subprocess
+import tempfile
+
+import pytest
+
+from compressed_latent_grouped_b200 import binding as B
+from rows_ref import config
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = 1 << 20      # an aligned address, never dereferenced on these paths
+
+
+def rows(ptr=P, batch=0, token=0, head=0):
+    return B.ccgqa_rows(ptr, batch, token, head)
+
+
+def test_struct_layouts_match_c():
+    names = {"ccgqa_rows": B.ccgqa_rows, "ccgqa_cache8": B.ccgqa_cache8, "ccgqa_append": B.ccgqa_append}
+    want = []
+    body = ""
+    for c, t in names.items():
+        body += f'printf("%zu ", sizeof({c}));'
+        want.append(ctypes.sizeof(t))
+        for f, _ in t._fields_:
+            body += f'printf("%zu ", offsetof({c}, {f}));'
+            want.append(getattr(t, f).offset)
+    with tempfile.TemporaryDirectory() as td:
+        src, exe = os.path.join(td, "l.c"), os.path.join(td, "l")
+        open(src, "w").write('#include <stdio.h>\n#include <stddef.h>\n#include "ccgqa.h"\n'
+                             "int main(void) {" + body + "return 0;}")
+        subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), src, "-o", exe], check=True)
+        got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == want
+
+
+def _append(lib, cfg, cache, c8=None, **kw):
+    d, n = 64, kw.pop("n", 4)
+    a = dict(q=rows(0), q_out=rows(0), k=rows(P, n * 2 * d, 2 * d, d), v=rows(P, n * 2 * d, 2 * d, d), k_out=rows(0),
+             n_valid=None, pos=None)
+    a.update(kw)
+    s = B.ccgqa_append(a["q"], a["q_out"], a["k"], a["v"], a["k_out"], n, a["n_valid"], a["pos"])
+    return B.ccgqa_kvcache_append_rope(cfg, cache, c8, s, stream=0, check=False)
+
+
+def _cache(cap=128, table=None, page=0, pages=0):
+    return B.ccgqa_kvcache(P, P, P, None, None, None, 3, cap, table, page, pages)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(k=rows(0)), 1), (dict(v=rows(0)), 1), (dict(k=rows(P + 2, 512, 128, 64)), 1),
+    (dict(k=rows(P, 512, 128, 60)), 1),              # heads overlap
+    (dict(k=rows(P, 512, 0, 64)), 1),                # broadcast tokens
+    (dict(k=rows(P, 512, -128, 64)), 1),
+    (dict(k=rows(P, 500, 128, 64)), 1),              # batches overlap, and not in 16 bytes
+    (dict(k=rows(P, 512, 128 + 4, 64)), 1),          # 8-byte stride
+    (dict(k=rows(P, 1 << 62, 128, 64)), 1),
+    (dict(q=rows(P, 2048, 512, 64)), 1),             # q without q_out
+    (dict(q_out=rows(P, 2048, 512, 64)), 1),
+    (dict(k_out=rows(P, 512, 128, 8)), 1),
+    (dict(n_valid=P + 2), 1), (dict(pos=P + 1), 1),
+    (dict(n=-1), 1), (dict(n=129), 3), (dict(n=0), 0),
+])
+def test_append_arguments(lib, kw, status):
+    assert _append(lib, config(8, 2, 64), _cache(), **kw) == status
+    assert B.ccgqa_launch_count() == 0
+
+
+@pytest.mark.parametrize("c8,cache,ok", [
+    ((3, 16, P, P), {}, False), ((0, 16, P, P), {}, False), ((1, 8, P, P), {}, False),
+    ((1, 48, P, P), {}, False), ((1, 256, P, P), {}, False), ((1, 16, 0, P), {}, False),
+    ((1, 16, P, P + 2), {}, False), ((2, 64, P, P), dict(cap=96), False),
+    ((2, 64, P, P), dict(table=P, page=32, pages=9), False),
+    ((1, 16, P, P), {}, True), ((2, 32, P + 4, P), dict(table=P, page=32, pages=9), True),
+])
+def test_cache8_arguments(lib, c8, cache, ok):
+    s = B.ccgqa_cache8(*c8[:2], *c8[2:])
+    cfg, c = config(8, 2, 64), _cache(**cache)
+    # n = 0 ends a good call before any launch
+    assert _append(lib, cfg, c, s, n=0) == (0 if ok else 1)
+    f = lambda n: B.ccgqa_kvcache_read(cfg, c, s, 0, n, rows(), rows(), stream=0, check=False)  # noqa: E731
+    assert f(0) == (0 if ok else 1)
+
+
+def test_read_arguments(lib):
+    cfg, c = config(8, 2, 64), _cache()
+    good = rows(P, 2 * 8 * 64, 64, 8 * 64)          # the cache's own order
+    f = lambda first, n, k, v: B.ccgqa_kvcache_read(cfg, c, None, first, n, k, v, stream=0, check=False)  # noqa: E731
+    assert f(-1, 8, good, good) == 1 and f(0, -1, good, good) == 1
+    assert f(121, 8, good, good) == 3 and f(1, 2 ** 31 - 1, good, good) == 3
+    assert f(0, 8, rows(0), good) == 1 and f(0, 8, good, rows(P, 2 * 8 * 64, 64, 7 * 64)) == 1
+    assert B.ccgqa_launch_count() == 0
