@@ -64,6 +64,10 @@ class ccgqa_append(ctypes.Structure):
                 ("pos", c_void_p)]
 
 
+class ccgqa_window(ctypes.Structure):
+    _fields_ = [("window", c_int32), ("sinks", c_int32)]
+
+
 class CCGQAError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -121,6 +125,12 @@ def load() -> ctypes.CDLL:
     lib.ccgqa_kvcache_read.argtypes = [P(ccgqa_config), P(ccgqa_kvcache), P(ccgqa_cache8), c_int32,
                                        c_int32, P(ccgqa_rows), P(ccgqa_rows), c_void_p, c_void_p]
     lib.ccgqa_kvcache_read.restype = c_int
+    lib.ccgqa_cache_attention_workspace_size.argtypes = [P(ccgqa_config), c_int32, c_int32]
+    lib.ccgqa_cache_attention_workspace_size.restype = c_size_t
+    lib.ccgqa_cache_attention.argtypes = [P(ccgqa_config), P(ccgqa_window), P(ccgqa_kvcache),
+                                          P(ccgqa_cache8), c_void_p, c_void_p, c_void_p, c_size_t,
+                                          c_void_p, c_void_p]
+    lib.ccgqa_cache_attention.restype = c_int
     lib.ccgqa_status_string.argtypes = [c_int]
     lib.ccgqa_status_string.restype = c_char_p
     lib.ccgqa_launch_count.argtypes = []
@@ -330,6 +340,21 @@ def ccgqa_kvcache_read(cfg, cache, cache8, first, n, k_out: ccgqa_rows, v_out: c
                                    _stream(stream))
     if check and st != 0:
         raise CCGQAError(st, "ccgqa_kvcache_read")
+    return st
+
+
+def ccgqa_cache_attention_workspace_size(cfg: ccgqa_config, batch: int, cap: int) -> int:
+    return int(load().ccgqa_cache_attention_workspace_size(ctypes.byref(cfg), batch, cap))
+
+
+def ccgqa_cache_attention(cfg, window, cache, cache8, q, out, workspace, dev_err=None, stream=None,
+                          check=True) -> int:
+    st = load().ccgqa_cache_attention(ctypes.byref(cfg), _ref(window), ctypes.byref(cache),
+                                      _ref(cache8), _ptr(q), _ptr(out), _ptr(workspace),
+                                      0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                      _ptr(dev_err), _stream(stream))
+    if check and st != 0:
+        raise CCGQAError(st, "ccgqa_cache_attention")
     return st
 
 

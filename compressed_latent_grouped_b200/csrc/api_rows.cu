@@ -1,6 +1,7 @@
 // C ABI of the operators on finished query / key / value rows: the append with
-// the rotation and the cache read-back.  Host-side validation and dispatch, as
-// in api.cu: nothing is launched on a bad argument.
+// the rotation, the cache read-back and the one-token attention over the cache.
+// Host-side validation and dispatch, as in api.cu: nothing is launched on a bad
+// argument.
 #include <algorithm>
 
 #include "api_internal.h"
@@ -85,6 +86,18 @@ cudaError_t run_append(const Geo& g, const ccgqa_kvcache* c, const ccgqa_cache8*
   return launch_append_rope<T>(x, c8 ? c8->format : 0, st);
 }
 
+// Chunks of query heads that one CTA of the cache attention takes.
+int64_t attn_units(const Geo& g, int64_t batch) {
+  const int per = g.dtype == CCGQA_BF16 ? kCacheAttnHeads : kCacheAttnHeadsF32;
+  return batch * g.Hkv * ((g.G + per - 1) / per);
+}
+size_t attn_workspace(const Geo& g, int64_t batch, int splits) {
+  if (splits == 1) return 0;
+  const int64_t rows = attn_units(g, batch) * splits * (g.dtype == CCGQA_BF16 ? kCacheAttnHeads : kCacheAttnHeadsF32);
+  return static_cast<size_t>(rows) * (g.d + 2) * sizeof(float);
+}
+bool window_ok(const ccgqa_window* w) { return !w || (w->window >= 0 && w->sinks >= 0); }
+
 }  // namespace
 }  // namespace ccgqa
 
@@ -155,5 +168,62 @@ CCGQA_API ccgqa_status ccgqa_kvcache_read(const ccgqa_config* cfg, const ccgqa_k
   const int fmt = c8 ? c8->format : 0;
   const cudaError_t e =
       g.dtype == CCGQA_BF16 ? launch_kv_read<bf16>(a, fmt, st) : launch_kv_read<float>(a, fmt, st);
+  return e == cudaSuccess ? CCGQA_OK : cuda_fail(e);
+}
+
+CCGQA_API size_t ccgqa_cache_attention_workspace_size(const ccgqa_config* cfg, int32_t batch,
+                                                      int32_t cap) {
+  Geo g;
+  if (derive(cfg, &g) != CCGQA_OK || batch <= 0 || cap <= 0) return 0;
+  return attn_workspace(g, batch, cache_attn_splits(attn_units(g, batch), cap));
+}
+
+CCGQA_API ccgqa_status ccgqa_cache_attention(const ccgqa_config* cfg, const ccgqa_window* win,
+                                             const ccgqa_kvcache* cache, const ccgqa_cache8* c8,
+                                             const void* q, void* out, void* workspace,
+                                             size_t workspace_bytes, int32_t* dev_err,
+                                             void* stream) {
+  Geo g;
+  ccgqa_status s = derive(cfg, &g);
+  if (s != CCGQA_OK) return s;
+  if ((s = check_cache(g, cache, false)) != CCGQA_OK) return s;
+  if ((s = check_cache8(cache, c8)) != CCGQA_OK) return s;
+  if (!window_ok(win) || !q || !out || !aligned16(q) || !aligned16(out)) return CCGQA_ERR_INVALID_ARG;
+  const int64_t units = attn_units(g, cache->batch);
+  if (units > 0x7fffffff / kCacheAttnMaxSplits) return CCGQA_ERR_UNSUPPORTED;
+  CacheAttnArgs a{};
+  a.window = win ? win->window : 0;
+  a.sinks = a.window ? win->sinks : 0;
+  // the tiles that hold a window and its sinks, at most two partly used each
+  const int64_t keys = a.window ? std::min<int64_t>(cache->cap, static_cast<int64_t>(a.window) + a.sinks + 64)
+                                : cache->cap;
+  a.splits = cache_attn_splits(units, keys);
+  const size_t need = attn_workspace(g, cache->batch, a.splits);
+  if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return CCGQA_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!stream_allowed(st)) return CCGQA_ERR_INVALID_ARG;
+  a.q = q;
+  a.ck = cache->k;
+  a.cv = cache->v;
+  if (c8) {
+    a.k_scale = c8->k_scale;
+    a.v_scale = c8->v_scale;
+    a.block_shift = log2_of(c8->block);
+  }
+  a.pages = page_map(cache);
+  a.len = cache->len;
+  a.cap = cache->cap;
+  a.B = cache->batch;
+  a.Hq = g.Hq;
+  a.Hkv = g.Hkv;
+  a.d = g.d;
+  a.G = g.G;
+  a.out = out;
+  a.part = static_cast<float*>(workspace);
+  a.part_ml = a.part + need / sizeof(float) / (g.d + 2) * g.d;
+  a.dev_err = dev_err;
+  const int fmt = c8 ? c8->format : 0;
+  const cudaError_t e = g.dtype == CCGQA_BF16 ? launch_cache_attn<bf16>(a, fmt, st)
+                                              : launch_cache_attn<float>(a, fmt, st);
   return e == cudaSuccess ? CCGQA_OK : cuda_fail(e);
 }

@@ -1,0 +1,794 @@
+// Attention of one query token per sequence over the tokens a cache holds
+// ("Grouped Query Attention (GQA)", "Por qué GQA reduce la caché KV": decode is
+// bound by reading the cache), for caches in the working type or in 8 bits
+// with a scale per block of tokens and kv head, over the whole sequence or over
+// the last `window` tokens and the first `sinks`:
+//   o = sum_s 2^(x_s - m) sv_s v_s / sum_s 2^(x_s - m),
+//   x_s = log2(e) / sqrt(d) * sk_s (q . k_s),   m = a running max of x.
+//
+// bf16 layers.  One CTA = a split of the visible tokens of one (sequence, kv
+// head, chunk of 16 query heads); its four warps take tiles of 16 or 32 tokens
+// in turn and never wait for one another: each warp copies its own tiles with
+// cp.async into a ring of its own, so a byte is read from memory once, for all
+// the heads of the group, and the loads of the next tiles are in flight while a
+// tile is worked.
+// The products run on mma.sync (m16n8k16, heads x tokens x d and heads x d x
+// tokens), not tcgen05: the codes have to pass through registers to become
+// 16-bit floats, and there they already are the fragments the instruction
+// reads; tcgen05 would want them written back to shared memory first, and the
+// group's few heads leave either engine nearly idle.
+//   S = Q K^T   thread (r, c) = (lane / 4, lane % 4) reads 16 contiguous bytes
+//               of token r, and those are its k-slots of consecutive steps: the
+//               d axis is summed over, so any order serves as long as Q's
+//               fragments use the same.
+//   O += P V    the scores leave S in the layout the next product wants P in.
+//               V's fragment pairs two tokens of one channel: a byte permute of
+//               the two tokens' words, then the conversion.
+// int8 codes become fp16 exactly by placing the byte (plus 128) in the mantissa
+// of 1024 and subtracting 1152; e4m3 codes by the hardware's conversion.  q is
+// scaled by a power of two per head into fp16's range (exact for all but
+// elements 2^-28 below the largest), the probabilities, times their block's v
+// scale, are rounded to fp16 after a second running max, of x + log2 sv, has
+// brought them near one.  Against a cache in bf16 both stay in bf16.
+//
+// fp32 layers.  CUDA cores, fp32 throughout, chunks of four query heads: d / 4
+// lanes share a token, each with four channels.
+//
+// Splits leave (numerators, max, sum) in the workspace and a second kernel
+// joins them; with one split the result is written at once.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "cache_codes.cuh"
+#include "sm100.cuh"
+
+namespace ccgqa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kCaThreads = kWarps * 32;
+constexpr float kLog2eC = 1.4426950408889634f;
+// The running maxima are raised when a weight passes 2^kLag.
+constexpr float kLag = 8.0f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
+
+// ----------------------------------------------------------------- visible tokens
+// The tokens the query at position L - 1 sees, as tiles of kTile tokens: the
+// sinks' tiles, then the window's.
+template <int kTile>
+struct Visible {
+  int L, lo, sinks;   // s < L and (s >= lo or s < sinks)
+  int n_sink, first, n;
+  __device__ __forceinline__ Visible(int len, int window, int n_sinks) {
+    L = len;
+    lo = window > 0 && len > window ? len - window : 0;
+    sinks = lo > 0 ? min(n_sinks, lo) : 0;
+    first = lo / kTile;
+    n_sink = min((sinks + kTile - 1) / kTile, first);
+    n = n_sink + (L + kTile - 1) / kTile - first;
+    if (L <= 0) n = 0;
+  }
+  __device__ __forceinline__ int start(int i) const { return (i < n_sink ? i : first + i - n_sink) * kTile; }
+  __device__ __forceinline__ bool sees(int s) const { return s < L && (s >= lo || s < sinks); }
+  __device__ __forceinline__ bool any(int s, int e) const { return s < L && (e > lo || s < sinks); }
+  __device__ __forceinline__ bool all(int s, int e) const { return e <= L && (s >= lo || e <= sinks); }
+};
+
+// Length of sequence b; zero, and an error bit, when it is outside [0, cap].
+__device__ __forceinline__ int checked_len(const CacheAttnArgs& a, int b, bool report) {
+  const int L = __ldg(a.len + b);
+  if (L >= 0 && L <= a.cap) return L;
+  if (report) raise_dev_err(a.dev_err, CCGQA_DEVERR_CAPACITY);
+  return 0;
+}
+
+// Row of the cache of token t (the start of 16 tokens), -1 for a bad page.
+__device__ __forceinline__ int64_t row_of(const CacheAttnArgs& a, int b, int g, int t) {
+  return kv_row(a.pages, b, g, a.Hkv, a.cap, t);
+}
+
+// ----------------------------------------------------------------- conversions
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  return __byte_perm(a, b, sel);
+}
+// Four codes -> two pairs of fp16.
+template <int FMT>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& h01, uint32_t& h23) {
+  if constexpr (FMT == kCacheI8) {
+    w ^= 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
+    uint32_t a = prmt(w, 0x64646464u, 0x4140), b = prmt(w, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+    h01 = *reinterpret_cast<const uint32_t*>(&x);
+    h23 = *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(h01), "=r"(h23)
+        : "r"(w));
+  }
+}
+
+template <bool kHalf>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (kHalf) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// D += A B, 16 x 16 by 16 x 8, fp32 sums.  kTop: rows 8..15 of A are zero and
+// their sums are not kept.
+template <bool kHalf, bool kTop>
+__device__ __forceinline__ void mma16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (kTop) {
+    float u, v;
+    if constexpr (kHalf)
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%8,%5,%8}, {%6,%7}, "
+          "{%0,%1,%9,%9};"
+          : "+f"(d[0]), "+f"(d[1]), "=f"(u), "=f"(v)
+          : "r"(a[0]), "r"(a[1]), "r"(b0), "r"(b1), "r"(0), "f"(0.f));
+    else
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%8,%5,%8}, {%6,%7}, "
+          "{%0,%1,%9,%9};"
+          : "+f"(d[0]), "+f"(d[1]), "=f"(u), "=f"(v)
+          : "r"(a[0]), "r"(a[1]), "r"(b0), "r"(b1), "r"(0), "f"(0.f));
+  } else {
+    if constexpr (kHalf)
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+          "{%0,%1,%2,%3};"
+          : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+      asm volatile(
+          "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+          "{%0,%1,%2,%3};"
+          : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+          : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+
+// Copy of 16 or 4 bytes to shared memory; zeros when !on.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// N bytes (4, 8 or 16) of shared memory as words.
+template <int N>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t* w) {
+  if constexpr (N == 16)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+  else if constexpr (N == 8)
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else if constexpr (N == 4)
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+  else
+    asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(w[0]) : "r"(addr));
+}
+
+template <int D, int FMT>
+struct CaCfg {
+  static constexpr int kEs = FMT == 0 ? 2 : 1;
+  static constexpr int kRow = D * kEs;                       // bytes of a token
+  static constexpr int kTile = kRow >= 128 ? 16 : 32;        // 4 KB of K and V at the common sizes
+  static constexpr int kStages = 3;
+  static constexpr int kMeta = FMT == 0 ? 0 : 16;            // k, v scales of the tile's two 16-token halves
+  static constexpr uint32_t kStage = 2 * kTile * kRow + kMeta;
+  static constexpr uint32_t kRing = kStages * kStage;        // per warp
+  static constexpr size_t kSmem = kWarps * kRing;
+  static constexpr int kPieceK = kRow / 4 < 16 ? kRow / 4 : 16;   // bytes of a token one thread reads at once
+  static constexpr int kPieceV = kRow / 8 < 16 ? kRow / 8 : 16;
+  static constexpr int kPiecesK = kRow / 4 / kPieceK;
+  static constexpr int kPiecesV = kRow / 8 / kPieceV;
+  // Shared-memory offset of byte x (of a 16-byte unit's row) of token `row`:
+  // 16-byte units are exchanged inside 128-byte lines so that both access
+  // patterns, tokens r with units c and tokens 2c with units r, are free of
+  // bank conflicts.
+  __device__ static __forceinline__ uint32_t at(int row, int byte) {
+    uint32_t x;
+    if constexpr (kRow >= 128) x = ((row >> 1) & 3) * 2 ^ (row & 1) * 4;
+    else if constexpr (kRow == 64) x = ((row >> 1) & 3) * 2;
+    else if constexpr (kRow == 32) x = ((row >> 2) & 1) * 2;
+    else x = 0;
+    return static_cast<uint32_t>(row * kRow + byte) ^ (x << 4);
+  }
+};
+
+// MR: 1 for at most 8 query heads in the chunk, 2 for 16.
+template <int D, int FMT, int MR>
+__global__ void __launch_bounds__(kCaThreads, (D == 128 || MR == 2) ? 2 : (D == 64 ? 3 : 4))
+    cache_attn_kernel(const CacheAttnArgs a) {
+  pdl_enter();
+  using C = CaCfg<D, FMT>;
+  constexpr bool kHalf = FMT != 0, kTop = MR == 1;
+  constexpr int NT = C::kTile / 8, KS = D / 16, NV = D / 8, kA = MR == 1 ? 2 : 4;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int chunks = (a.G + kCacheAttnHeads - 1) / kCacheAttnHeads;
+  const int unit = blockIdx.x / a.splits, sp = blockIdx.x - unit * a.splits;
+  const int hc = unit % chunks, g = unit / chunks % a.Hkv, b = unit / chunks / a.Hkv;
+  const int heads = min(a.G - hc * kCacheAttnHeads, kCacheAttnHeads);
+  const int h0 = g * a.G + hc * kCacheAttnHeads;
+  const int L = checked_len(a, b, g == 0 && hc == 0 && sp == 0 && threadIdx.x == 0);
+  const Visible<C::kTile> vis(L, a.window, a.sinks);
+  const int i0 = static_cast<int>(static_cast<int64_t>(vis.n) * sp / a.splits);
+  const int i1 = static_cast<int>(static_cast<int64_t>(vis.n) * (sp + 1) / a.splits);
+  uint8_t* ring = smem + warp * C::kRing;
+  const uint32_t ring_s = sm100::smem_addr(ring);
+
+  // ---- the ring: tile i of this warp into stage st
+  int64_t row0 = 0, row1 = 0;   // cache rows of the next tile's 16-token halves
+  int next = i0 + warp, bad = 0;   // bad: two bits a stage, halves whose page is not in the pool
+  auto locate = [&](int i) {
+    if (i >= i1) return;
+    const int t0 = vis.start(i);
+    row0 = vis.any(t0, t0 + 16) ? row_of(a, b, g, t0) : -2;
+    if constexpr (C::kTile == 32) row1 = vis.any(t0 + 16, t0 + 32) ? row_of(a, b, g, t0 + 16) : -2;
+  };
+  auto load = [&](int i, int st) {
+    if (i < i1) {
+      const int t0 = vis.start(i);
+      const uint32_t base = ring_s + st * C::kStage;
+      constexpr int kUnits = C::kRow / 16;
+#pragma unroll
+      for (int x = 0; x < C::kTile * kUnits / 32; ++x) {
+        const int idx = lane + 32 * x, row = idx / kUnits, u = idx % kUnits;
+        const int64_t rb = row < 16 ? row0 : row1;
+        const bool on = rb >= 0 && vis.sees(t0 + row);
+        const int64_t off = on ? (rb + (row & 15)) * C::kRow + u * 16 : 0;
+        const uint32_t dst = base + C::at(row, u * 16);
+        copy16(dst, static_cast<const uint8_t*>(a.ck) + off, on);
+        copy16(dst + C::kTile * C::kRow, static_cast<const uint8_t*>(a.cv) + off, on);
+      }
+      if (FMT != 0 && lane < 4) {
+        const int64_t rb = (lane & 1) == 0 ? row0 : (C::kTile == 32 ? row1 : -2);
+        const float* sc = lane < 2 ? a.k_scale : a.v_scale;
+        copy4(base + 2 * C::kTile * C::kRow + lane * 4, sc + (rb >= 0 ? rb >> a.block_shift : 0), rb >= 0);
+      }
+      const int bits = (row0 == -1 ? 1 : 0) | (C::kTile == 32 && row1 == -1 ? 2 : 0);
+      bad = (bad & ~(3 << (2 * st))) | bits << (2 * st);
+      if (bits && lane == 0) raise_dev_err(a.dev_err, CCGQA_DEVERR_INDEX);
+    }
+    sm100::cp_async_commit_group();
+  };
+  locate(next);
+#pragma unroll
+  for (int st = 0; st < C::kStages - 1; ++st) {
+    load(next, st);
+    next += kWarps;
+    locate(next);
+  }
+
+  // ---- Q fragments: head r (and r + 8), channels in the order of K's pieces
+  uint32_t qf[KS][kA];
+  float cs[MR];   // score of an accumulator, in units of log2
+#pragma unroll
+  for (int m = 0; m < MR; ++m) {
+    const int h = r + 8 * m;
+    const bf16* q = static_cast<const bf16*>(a.q) + (static_cast<int64_t>(b) * a.Hq + h0 + h) * D;
+    constexpr int kEl = C::kPieceK / C::kEs;   // channels of a piece
+    uint2 w[KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const int ch = (c + 4 * (k * 4 / kEl)) * kEl + k * 4 % kEl;
+      w[k] = h < heads ? *reinterpret_cast<const uint2*>(q + ch) : make_uint2(0, 0);
+    }
+    cs[m] = kLog2eC * rsqrtf(static_cast<float>(D));
+    if constexpr (kHalf) {
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const float2 x = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[k].x));
+        const float2 y = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[k].y));
+        top = fmaxf(top, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // largest element to [2^14, 2^15); zero, tiny and infinite ones keep a finite scale
+      int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xffu) - 127;
+      e = min(max(e, -100), 126);
+      const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+      cs[m] *= __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const float2 x = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[k].x));
+        const float2 y = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[k].y));
+        w[k] = make_uint2(pack16<true>(x.x * up, x.y * up), pack16<true>(y.x * up, y.y * up));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      // A's registers: (row r, k lo), (row r + 8, k lo), (r, k hi), (r + 8, k hi)
+      qf[k][MR == 1 ? 0 : m] = w[k].x;
+      qf[k][MR == 1 ? 1 : 2 + m] = w[k].y;
+    }
+  }
+
+  float o[NV][2 * MR];
+  float m_run[MR], w_max[MR], w_exp[MR], l[MR];   // max of x, of x + log2 sv; the weights' power of two; sum
+#pragma unroll
+  for (int m = 0; m < MR; ++m) {
+    m_run[m] = w_max[m] = -INFINITY;
+    w_exp[m] = l[m] = 0.f;
+  }
+#pragma unroll
+  for (int t = 0; t < NV; ++t)
+#pragma unroll
+    for (int e = 0; e < 2 * MR; ++e) o[t][e] = 0.f;
+
+  int st = 0;
+  for (int i = i0 + warp; i < i1; i += kWarps) {
+    copies_wait<C::kStages - 2>();
+    __syncwarp();
+    load(next, st == 0 ? C::kStages - 1 : st - 1);
+    next += kWarps;
+    locate(next);
+    const int t0 = vis.start(i);
+    const uint32_t kt = ring_s + st * C::kStage, vt = kt + C::kTile * C::kRow;
+
+    // S = Q K^T
+    float s[NT][2 * MR];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int e = 0; e < 2 * MR; ++e) s[j][e] = 0.f;
+#pragma unroll
+      for (int u = 0; u < C::kPiecesK; ++u) {
+        uint32_t w[4];
+        lds<C::kPieceK>(kt + C::at(8 * j + r, (c + 4 * u) * C::kPieceK), w);
+        constexpr int kSteps = C::kPieceK / C::kEs / 4;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t b0, b1;
+          if constexpr (FMT == 0) {
+            b0 = w[2 * k];
+            b1 = w[2 * k + 1];
+          } else {
+            codes_to_half<FMT>(w[k], b0, b1);
+          }
+          mma16<kHalf, kTop>(s[j], qf[u * kSteps + k], b0, b1);
+        }
+      }
+    }
+
+    // scores, masks, running maxima
+    float sk[2] = {1.f, 1.f}, sv[2] = {1.f, 1.f}, lsv[2] = {0.f, 0.f};
+    if constexpr (FMT != 0) {
+      uint32_t w[4];
+      lds<16>(kt + 2 * C::kTile * C::kRow, w);
+      sk[0] = __uint_as_float(w[0]);
+      sk[1] = __uint_as_float(w[1]);
+      sv[0] = __uint_as_float(w[2]);
+      sv[1] = __uint_as_float(w[3]);
+      lsv[0] = __log2f(fabsf(sv[0]));
+      lsv[1] = __log2f(fabsf(sv[1]));
+    }
+    const int bits = (bad >> (2 * st)) & 3;
+    const bool whole = bits == 0 && vis.all(t0, t0 + C::kTile);
+    float mx[MR], wx[MR];
+#pragma unroll
+    for (int m = 0; m < MR; ++m) mx[m] = wx[m] = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int m = 0; m < MR; ++m) {
+        const float f = FMT == 0 ? cs[m] : cs[m] * sk[j >> 1];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = s[j][2 * m + e] * f;
+          if (!whole && (!vis.sees(t0 + 8 * j + 2 * c + e) || ((bits >> (j >> 1)) & 1))) x = -INFINITY;
+          s[j][2 * m + e] = x;
+          mx[m] = fmaxf(mx[m], x);
+          if constexpr (FMT != 0) wx[m] = fmaxf(wx[m], x + lsv[j >> 1]);
+        }
+      }
+    }
+    bool raise = false;
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+      raise |= mx[m] > m_run[m] + kLag;
+      if constexpr (FMT != 0) raise |= wx[m] > w_max[m] + kLag;
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int m = 0; m < MR; ++m) {
+        mx[m] = fmaxf(mx[m], __shfl_xor_sync(0xffffffffu, mx[m], 1));
+        mx[m] = fmaxf(mx[m], __shfl_xor_sync(0xffffffffu, mx[m], 2));
+        const float m_old = m_run[m], e_old = w_exp[m];
+        m_run[m] = fmaxf(m_run[m], mx[m]);
+        if constexpr (FMT != 0) {
+          wx[m] = fmaxf(wx[m], __shfl_xor_sync(0xffffffffu, wx[m], 1));
+          wx[m] = fmaxf(wx[m], __shfl_xor_sync(0xffffffffu, wx[m], 2));
+          w_max[m] = fmaxf(w_max[m], wx[m]);
+          if (w_max[m] > -INFINITY) w_exp[m] = fminf(fmaxf(rintf(m_run[m] - w_max[m]), -126.f), 126.f);
+        }
+        // sums so far are in units of 2^-m_old (and the weights' 2^e_old)
+        const float fl = m_old == -INFINITY ? 1.f : exp2_approx(m_old - m_run[m]);
+        const float fo = m_old == -INFINITY ? 1.f : exp2_approx(m_old - m_run[m] + (w_exp[m] - e_old));
+        l[m] *= fl;
+#pragma unroll
+        for (int t = 0; t < NV; ++t) {
+          o[t][2 * m] *= fo;
+          o[t][2 * m + 1] *= fo;
+        }
+      }
+    }
+    uint32_t p[NT / 2][kA];
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+      const float base = finite_or_zero(m_run[m]);
+      float f[2] = {1.f, 1.f};
+      if constexpr (FMT != 0) {
+        const float up = exp2_approx(w_exp[m]);
+        f[0] = sv[0] * up;
+        f[1] = sv[1] * up;
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float x = exp2_approx(s[j][2 * m] - base), y = exp2_approx(s[j][2 * m + 1] - base);
+        l[m] += x + y;
+        if constexpr (FMT != 0) {
+          // masked tokens weigh nothing, whatever their block's scale
+          x = x == 0.f ? 0.f : x * f[j >> 1];
+          y = y == 0.f ? 0.f : y * f[j >> 1];
+        }
+        p[j >> 1][MR == 1 ? (j & 1) : (j & 1) * 2 + m] = pack16<kHalf>(x, y);
+      }
+    }
+
+    // O += P V
+#pragma unroll
+    for (int ks = 0; ks < NT / 2; ++ks) {
+#pragma unroll
+      for (int u = 0; u < C::kPiecesV; ++u) {
+        uint32_t w[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          lds<C::kPieceV>(vt + C::at(16 * ks + 2 * c + (q & 1) + (q >> 1) * 8, (r + 8 * u) * C::kPieceV), w[q]);
+        constexpr int kEl = C::kPieceV / C::kEs;
+        if constexpr (FMT == 0) {
+#pragma unroll
+          for (int e = 0; e < kEl; ++e) {
+            const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
+            mma16<false, kTop>(o[u * kEl + e], p[ks], prmt(w[0][e >> 1], w[1][e >> 1], sel),
+                               prmt(w[2][e >> 1], w[3][e >> 1], sel));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kEl; e += 2) {
+            const uint32_t sel = e & 2 ? 0x7362 : 0x5140;
+            uint32_t b0[2], b1[2];
+            codes_to_half<FMT>(prmt(w[0][e >> 2], w[1][e >> 2], sel), b0[0], b0[1]);
+            codes_to_half<FMT>(prmt(w[2][e >> 2], w[3][e >> 2], sel), b1[0], b1[1]);
+            mma16<true, kTop>(o[u * kEl + e], p[ks], b0[0], b1[0]);
+            mma16<true, kTop>(o[u * kEl + e + 1], p[ks], b0[1], b1[1]);
+          }
+        }
+      }
+    }
+    st = st + 1 == C::kStages ? 0 : st + 1;
+  }
+
+  // ---- join the warps: each leaves its numerators, max and sum in shared memory
+  copies_wait<0>();
+  __syncthreads();
+  constexpr int kRows = 8 * MR;
+  float* num = reinterpret_cast<float*>(smem);            // [warp][row][D]
+  float* ml = num + kWarps * kRows * D;                   // [warp][row][2]
+#pragma unroll
+  for (int m = 0; m < MR; ++m) {
+    l[m] += __shfl_xor_sync(0xffffffffu, l[m], 1);
+    l[m] += __shfl_xor_sync(0xffffffffu, l[m], 2);
+    const int row = warp * kRows + 8 * m + r;
+    if (c == 0) {
+      ml[row * 2] = l[m] == 0.f ? -INFINITY : finite_or_zero(m_run[m]);   // NaN scores alone leave no max
+      ml[row * 2 + 1] = l[m];
+    }
+    const float back = exp2_approx(-w_exp[m]);
+    constexpr int kEl = C::kPieceV / C::kEs;
+#pragma unroll
+    for (int u = 0; u < C::kPiecesV; ++u)
+#pragma unroll
+      for (int e = 0; e < kEl; ++e)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          num[row * D + (2 * c + y + 8 * u) * kEl + e] = o[u * kEl + e][2 * m + y] * back;
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < heads * D; x += kCaThreads) {
+    const int h = x / D, e = x - h * D;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[(w * kRows + h) * 2]);
+    float sum = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = ml[(w * kRows + h) * 2];
+      if (mw == -INFINITY) continue;
+      const float f = exp2_approx(mw - top);
+      sum += ml[(w * kRows + h) * 2 + 1] * f;
+      acc += num[(w * kRows + h) * D + e] * f;
+    }
+    if (a.splits == 1) {
+      static_cast<bf16*>(a.out)[(static_cast<int64_t>(b) * a.Hq + h0 + h) * D + e] =
+          __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
+    } else {
+      const int64_t row = static_cast<int64_t>(blockIdx.x) * kCacheAttnHeads + h;
+      a.part[row * D + e] = acc;
+      if (e == 0) {
+        a.part_ml[row * 2] = top;
+        a.part_ml[row * 2 + 1] = sum;
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- fp32
+// D / 4 lanes share a token; a warp works 16 tokens at a time.
+template <int D, int FMT>
+__global__ void __launch_bounds__(kCaThreads)
+    cache_attn_f32_kernel(const CacheAttnArgs a) {
+  pdl_enter();
+  constexpr int LPK = D / 4, KPW = 32 / LPK, H = kCacheAttnHeadsF32;
+  constexpr int kSteps = 16 / KPW, U = kSteps < 8 ? kSteps : 8;   // tokens a lane group holds at once
+  __shared__ float num[kWarps * KPW][H][D];
+  __shared__ float ml[kWarps * KPW][H][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / LPK, e0 = lane % LPK * 4;
+  const int chunks = (a.G + H - 1) / H;
+  const int unit = blockIdx.x / a.splits, sp = blockIdx.x - unit * a.splits;
+  const int hc = unit % chunks, g = unit / chunks % a.Hkv, b = unit / chunks / a.Hkv;
+  const int heads = min(a.G - hc * H, H), h0 = g * a.G + hc * H;
+  const int L = checked_len(a, b, g == 0 && hc == 0 && sp == 0 && threadIdx.x == 0);
+  const Visible<16> vis(L, a.window, a.sinks);
+  const int i0 = static_cast<int>(static_cast<int64_t>(vis.n) * sp / a.splits);
+  const int i1 = static_cast<int>(static_cast<int64_t>(vis.n) * (sp + 1) / a.splits);
+  float q[H][4], o[H][4], m[H], l[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (h < heads)
+      x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.Hq + h0 + h) * D + e0);
+    q[h][0] = x.x;
+    q[h][1] = x.y;
+    q[h][2] = x.z;
+    q[h][3] = x.w;
+    m[h] = -INFINITY;
+    l[h] = o[h][0] = o[h][1] = o[h][2] = o[h][3] = 0.f;
+  }
+  const float cs = kLog2eC * rsqrtf(static_cast<float>(D));
+  auto fetch = [&](const void* base, int64_t row, float (&x)[4]) {
+    if constexpr (FMT == 0) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + row * D + e0));
+      x[0] = v.x;
+      x[1] = v.y;
+      x[2] = v.z;
+      x[3] = v.w;
+    } else {
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(base) + row * D + e0));
+      float y[8];
+      decode8<FMT>(make_uint2(w, 0), y);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = y[e];
+    }
+  };
+  for (int i = i0 + warp; i < i1; i += kWarps) {
+    const int t0 = vis.start(i);
+    const int64_t rb = row_of(a, b, g, t0);
+    if (rb < 0) {
+      if (lane == 0) raise_dev_err(a.dev_err, CCGQA_DEVERR_INDEX);
+      continue;
+    }
+    const float sk = FMT == 0 ? cs : cs * __ldg(a.k_scale + (rb >> a.block_shift));
+    const float sv = FMT == 0 ? 1.f : __ldg(a.v_scale + (rb >> a.block_shift));
+#pragma unroll
+    for (int u0 = 0; u0 < kSteps; u0 += U) {
+      float k[U][4], v[U][4];
+      bool on[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = (u0 + u) * KPW + grp;
+        on[u] = vis.sees(t0 + t);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) k[u][e] = v[u][e] = 0.f;
+        if (on[u]) {
+          fetch(a.ck, rb + t, k[u]);
+          fetch(a.cv, rb + t, v[u]);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        float x[U], top = m[h];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          x[u] = q[h][0] * k[u][0];
+#pragma unroll
+          for (int e = 1; e < 4; ++e) x[u] = fmaf(q[h][e], k[u][e], x[u]);
+        }
+#pragma unroll
+        for (int off = LPK / 2; off > 0; off >>= 1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) x[u] += __shfl_xor_sync(0xffffffffu, x[u], off);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          x[u] = on[u] ? x[u] * sk : -INFINITY;
+          top = fmaxf(top, x[u]);
+        }
+        const float base = finite_or_zero(top);
+        const float f = exp2f(finite_or_zero(m[h]) - base);   // sums are zero while there is no max
+        m[h] = top;
+        l[h] *= f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[h][e] *= f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (!on[u]) continue;
+          const float p = exp2f(x[u] - base), w = p * sv;
+          l[h] += p;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[h][e] = fmaf(w, v[u][e], o[h][e]);
+        }
+      }
+    }
+  }
+  // ---- join the lane groups
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    const int row = warp * KPW + grp;
+    *reinterpret_cast<float4*>(&num[row][h][e0]) = make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
+    if (e0 == 0) {
+      ml[row][h][0] = l[h] == 0.f ? -INFINITY : finite_or_zero(m[h]);
+      ml[row][h][1] = l[h];
+    }
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < heads * D; x += kCaThreads) {
+    const int h = x / D, e = x - h * D;
+    float top = -INFINITY, sum = 0.f, acc = 0.f;
+    for (int w = 0; w < kWarps * KPW; ++w) top = fmaxf(top, ml[w][h][0]);
+    for (int w = 0; w < kWarps * KPW; ++w) {
+      if (ml[w][h][0] == -INFINITY) continue;
+      const float f = exp2f(ml[w][h][0] - top);
+      sum = fmaf(ml[w][h][1], f, sum);
+      acc = fmaf(num[w][h][e], f, acc);
+    }
+    if (a.splits == 1) {
+      static_cast<float*>(a.out)[(static_cast<int64_t>(b) * a.Hq + h0 + h) * D + e] = sum == 0.f ? 0.f : acc / sum;
+    } else {
+      const int64_t row = static_cast<int64_t>(blockIdx.x) * H + h;
+      a.part[row * D + e] = acc;
+      if (e == 0) {
+        a.part_ml[row * 2] = top;
+        a.part_ml[row * 2 + 1] = sum;
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- join of the splits
+// One CTA per (sequence, kv head, chunk) and head of the chunk.
+template <typename T, int H>
+__global__ void __launch_bounds__(128) cache_attn_join_kernel(const CacheAttnArgs a) {
+  pdl_enter();
+  __shared__ float wt[kCacheAttnMaxSplits];
+  __shared__ float total;
+  const int chunks = (a.G + H - 1) / H;
+  const int unit = blockIdx.x / H, h = blockIdx.x % H;
+  const int hc = unit % chunks, g = unit / chunks % a.Hkv, b = unit / chunks / a.Hkv;
+  if (hc * H + h >= a.G) return;
+  const int64_t first = static_cast<int64_t>(unit) * a.splits * H + h;   // rows are H apart
+  if (threadIdx.x < 32) {
+    float top = -INFINITY, sum = 0.f;
+    for (int s = threadIdx.x; s < a.splits; s += 32) top = fmaxf(top, a.part_ml[(first + s * H) * 2]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    for (int s = threadIdx.x; s < a.splits; s += 32) {
+      const float m = a.part_ml[(first + s * H) * 2];
+      const float f = m == -INFINITY ? 0.f : exp2f(m - top);
+      wt[s] = f;
+      if (f != 0.f) sum = fmaf(a.part_ml[(first + s * H) * 2 + 1], f, sum);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (threadIdx.x == 0) total = sum;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.d; e += 128) {
+    float acc = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s)
+      if (wt[s] != 0.f) acc = fmaf(a.part[(first + s * H) * a.d + e], wt[s], acc);
+    static_cast<T*>(a.out)[(static_cast<int64_t>(b) * a.Hq + g * a.G + hc * H + h) * a.d + e] =
+        from_f32<T>(total == 0.f ? 0.f : acc / total);
+  }
+}
+
+template <typename T, int H>
+cudaError_t launch_join(const CacheAttnArgs& a, int units, cudaStream_t stream) {
+  if (a.splits == 1) return cudaGetLastError();
+  const cudaError_t e = launch_pdl(cache_attn_join_kernel<T, H>, dim3(units * H), dim3(128), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <int D, int FMT>
+cudaError_t launch_bf16(const CacheAttnArgs& a, cudaStream_t stream) {
+  using C = CaCfg<D, FMT>;
+  const int units = a.B * a.Hkv * ((a.G + kCacheAttnHeads - 1) / kCacheAttnHeads);
+  const bool wide = a.G > 8;
+  auto kernel = wide ? cache_attn_kernel<D, FMT, 2> : cache_attn_kernel<D, FMT, 1>;
+  const size_t join = static_cast<size_t>(kWarps) * (wide ? 16 : 8) * (D + 2) * sizeof(float);
+  const size_t smem = std::max(C::kSmem, join);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3(units * a.splits), dim3(kCaThreads), smem, stream, a);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  return launch_join<bf16, kCacheAttnHeads>(a, units, stream);
+}
+
+template <int D, int FMT>
+cudaError_t launch_f32(const CacheAttnArgs& a, cudaStream_t stream) {
+  const int units = a.B * a.Hkv * ((a.G + kCacheAttnHeadsF32 - 1) / kCacheAttnHeadsF32);
+  const cudaError_t e = launch_pdl(cache_attn_f32_kernel<D, FMT>, dim3(units * a.splits), dim3(kCaThreads), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  return launch_join<float, kCacheAttnHeadsF32>(a, units, stream);
+}
+
+template <typename T, int D>
+cudaError_t launch_fmt(const CacheAttnArgs& a, int fmt, cudaStream_t stream) {
+  constexpr bool kB = sizeof(T) == 2;
+  switch (fmt) {
+    case 0: return kB ? launch_bf16<D, 0>(a, stream) : launch_f32<D, 0>(a, stream);
+    case kCacheI8: return kB ? launch_bf16<D, kCacheI8>(a, stream) : launch_f32<D, kCacheI8>(a, stream);
+    case kCacheE4M3: return kB ? launch_bf16<D, kCacheE4M3>(a, stream) : launch_f32<D, kCacheE4M3>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+// Splits so that a few waves of CTAs cover the GPU, each with a few tiles per
+// warp.
+int cache_attn_splits(int64_t units, int64_t keys) {
+  const int64_t want = (static_cast<int64_t>(sm_count()) * 8 + units - 1) / units;
+  const int64_t most = (keys + 511) / 512;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, kCacheAttnMaxSplits})));
+}
+
+template <typename T>
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, int fmt, cudaStream_t stream) {
+  switch (a.d) {
+    case 16: return launch_fmt<T, 16>(a, fmt, stream);
+    case 32: return launch_fmt<T, 32>(a, fmt, stream);
+    case 64: return launch_fmt<T, 64>(a, fmt, stream);
+    case 128: return launch_fmt<T, 128>(a, fmt, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+template cudaError_t launch_cache_attn<float>(const CacheAttnArgs&, int, cudaStream_t);
+template cudaError_t launch_cache_attn<bf16>(const CacheAttnArgs&, int, cudaStream_t);
+
+}  // namespace ccgqa

@@ -265,6 +265,30 @@ struct ReadArgs {
 template <typename T>
 cudaError_t launch_kv_read(const ReadArgs& a, int fmt, cudaStream_t stream);
 
+// One query token per sequence against the cache (ccgqa_cache_attention).
+struct CacheAttnArgs {
+  const void *q, *ck, *cv;      // q [B, Hq, d]
+  const float *k_scale, *v_scale;
+  int block_shift;
+  PageMap pages;
+  const int32_t* len;
+  int64_t cap;
+  int B, Hq, Hkv, d, G, window, sinks;   // window 0: the whole sequence
+  void* out;                    // [B, Hq, d]
+  int splits;                   // of the visible tokens of a (sequence, kv head, chunk of heads)
+  // partial results (splits > 1): numerators [unit][split][heads of a chunk][d],
+  // max and sum [unit][split][heads of a chunk][2]
+  float *part, *part_ml;
+  int32_t* dev_err;
+};
+constexpr int kCacheAttnHeads = 16, kCacheAttnHeadsF32 = 4;   // query heads of a chunk
+constexpr int kCacheAttnMaxSplits = 256;
+// Splits for `units` (sequence, kv head, chunk)s of at most `keys` visible
+// tokens; does not fall when keys grow.
+int cache_attn_splits(int64_t units, int64_t keys);
+template <typename T>
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, int fmt, cudaStream_t stream);
+
 // Split plan for the decode step, shared by the workspace-size query and the launch.
 void decode_plan(int B, int Hkv, int E, int N, int64_t cap, bool has_proj, int es,
                  int* e_splits, int* splits, int* chunk);

@@ -175,6 +175,19 @@ def _check_dense(where, name, t, shape, dtype, device, optional=False):
         _bad(where, f"{name} is not contiguous")
 
 
+def _workspace(nbytes: int, device, stream):
+    """Scratch of one call, from torch's allocator; handed back to it in the
+    order of the stream the call runs on."""
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def head_dim(cfg: B.ccgqa_config) -> int:
     return cfg.E // (cfg.C * cfg.n_q_heads)
 
@@ -262,6 +275,7 @@ class DeviceKVCache:
         self.block_table = block_table
         self.cache = B.make_kvcache(k, v, len_, block_table=block_table)
         self.dev_err = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._attn_ws = B.ccgqa_cache_attention_workspace_size(cfg, self.batch, self.cap)
 
     def append_rope(self, k, v, q=None, q_out=None, k_out=None, n_valid=None, pos=None, stream=None):
         """Append rows k, v [batch, n, Hkv, d], keys rotated; with q [batch, n,
@@ -308,6 +322,22 @@ class DeviceKVCache:
                                  B.make_rows(k_out, "bhtd"), B.make_rows(v_out, "bhtd"), self.dev_err,
                                  stream)
         return k_out, v_out
+
+    def attend(self, q, out=None, window: int = 0, sinks: int = 0, stream=None):
+        """One query token per sequence, q [batch, Hq, d] at position len - 1,
+        over the cached tokens (with ``window`` > 0 the last ``window`` and the
+        first ``sinks`` of them): out [batch, Hq, d].  Each call takes its
+        workspace from torch's allocator."""
+        shape = (self.batch, self.cfg.n_q_heads, self.d)
+        _check_dense("attend", "q", q, shape, self.dtype, self.device)
+        with torch.cuda.device(self.device):
+            if out is None:
+                out = torch.empty(shape, dtype=self.dtype, device=self.device)
+            _check_dense("attend", "out", out, shape, self.dtype, self.device)
+            ws = _workspace(self._attn_ws, self.device, stream)
+            B.ccgqa_cache_attention(self.cfg, B.ccgqa_window(window, sinks), self.cache, self.cache8, q, out,
+                                    ws, self.dev_err, stream)
+        return out
 
     def error_bits(self) -> int:
         return int(self.dev_err.item())

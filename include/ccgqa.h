@@ -311,7 +311,8 @@ CCGQA_API ccgqa_status ccgqa_output_projection(const ccgqa_config* cfg, const vo
 
 /* ---------------------------------------------------------------------------
  * Cache operators on rows that are already queries, keys and values (a plain
- * grouped-query layer, or one that makes its own rows).
+ * grouped-query layer, or one that makes its own rows): the append with the
+ * rotation and the one-token attention over the cache.
  * Of cfg they use E, C, n_q_heads, n_kv_heads (head dim d = E / (C Hq)), dtype
  * and, where stated, rope_base; cfg is validated as for every call.
  * ------------------------------------------------------------------------- */
@@ -390,6 +391,41 @@ CCGQA_API ccgqa_status ccgqa_kvcache_read(const ccgqa_config* cfg, const ccgqa_k
                                           const ccgqa_cache8* c8, int32_t first, int32_t n,
                                           const ccgqa_rows* k_out, const ccgqa_rows* v_out,
                                           int32_t* dev_err, void* stream);
+
+/* Which keys the query at position t sees: s <= t and, with window > 0, also
+ * t - window < s or s < sinks (the last `window` tokens, its own among them,
+ * and the first `sinks`).  window = 0: every s <= t (sinks is then ignored).
+ * Both >= 0.  A NULL ccgqa_window is {0, 0}. */
+typedef struct {
+  int32_t window;
+  int32_t sinks;
+} ccgqa_window;
+
+/* Workspace bytes of ccgqa_cache_attention for any window (0 on an invalid
+ * configuration, and where one CTA takes a whole sequence and no workspace is
+ * needed); 16-byte aligned, contents need no preparation. */
+CCGQA_API size_t ccgqa_cache_attention_workspace_size(const ccgqa_config* cfg, int32_t batch,
+                                                      int32_t cap);
+
+/* Attention of one query token per sequence, at position len[b] - 1, over the
+ * tokens the cache holds (append first, then attend):
+ *   out[b, h] = sum_s softmax_s(q[b, h] . k_s / sqrt(d)) v_s  over the visible s.
+ *  - q, out: [batch, Hq, d] dense, cfg->dtype.
+ *  - c8 NULL: k / v in cfg->dtype; otherwise codes with their scales.
+ *  - bf16: tensor-core products with fp32 sums (q in fp16 scaled by a power of
+ *    two and probabilities in fp16 against an 8-bit cache, both in bf16
+ *    against a bf16 cache); f32: fp32 throughout.
+ *  - len[b] == 0: the out row is zero.  len[b] outside [0, cap]: zero, and
+ *    CCGQA_DEVERR_CAPACITY.  A needed page id outside the pool sets
+ *    CCGQA_DEVERR_INDEX, its tokens count as absent.
+ *  - What masked tokens and rows past len[b] hold has no effect (NaN included).
+ * Nothing of the cache is written.  Calls that overlap on the GPU need
+ * workspaces of their own. */
+CCGQA_API ccgqa_status ccgqa_cache_attention(const ccgqa_config* cfg, const ccgqa_window* win,
+                                             const ccgqa_kvcache* cache, const ccgqa_cache8* c8,
+                                             const void* q, void* out, void* workspace,
+                                             size_t workspace_bytes, int32_t* dev_err,
+                                             void* stream);
 
 /* Static description of a status code. */
 CCGQA_API const char* ccgqa_status_string(ccgqa_status s);

@@ -68,3 +68,46 @@ def dense_rows(x, table):
         return x
     t = table.cpu().numpy()
     return np.stack([np.concatenate([x[p] for p in row], 1) for row in t])
+
+
+def cache_values(c, table=None):
+    """k, v of a DeviceKVCache as float64 [batch, Hkv, cap, d]."""
+    out = []
+    for name in ("k", "v"):
+        x = dense_rows(getattr(c, name), table)
+        if c.block:
+            x = x * np.repeat(dense_rows(getattr(c, name + "_scale"), table), c.block, 2)[..., None]
+        out.append(x)
+    return out
+
+
+def seen(t, s, window, sinks):
+    """Whether the query at position t sees key s (broadcast)."""
+    ok = s <= t
+    return ok & ((s > t - window) | (s < sinks)) if window else ok
+
+
+def attend(q, k, v, keys):
+    """One query row per head over the listed keys: q [Hq, d], k, v [Hkv, cap, d].
+    Returns (out, weighted |v|, largest sum |q_i k_i| / sqrt(d))."""
+    Hq, d = q.shape
+    G = Hq // k.shape[0]
+    out, mag, top = np.zeros((Hq, d)), np.zeros((Hq, d)), 0.0
+    for h in range(Hq):
+        if len(keys) == 0:
+            continue
+        kk, vv = k[h // G, keys], v[h // G, keys]
+        s = kk @ q[h] / np.sqrt(d)
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        out[h], mag[h] = p @ vv, p @ np.abs(vv)
+        top = max(top, (np.abs(kk) @ np.abs(q[h])).max() / np.sqrt(d))
+    return out, mag, top
+
+
+def attention_slack(d, n, top):
+    """Relative error of softmax sums in fp32: scores are off by (d + 3) 2^-24
+    of sum |q k| / sqrt(d) (in the exponent), in the numerator and in the
+    denominator; sums over n terms by n 2^-24 each; exponentials (in base 2, an
+    argument of up to 2 top log2 e rounded to 2^-24, and the hardware's 2^-22)."""
+    return 2 * (d + 3 + 4) * 2.0 ** -24 * top + (2 * n + 32) * 2.0 ** -24

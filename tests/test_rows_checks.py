@@ -93,3 +93,27 @@ def test_read_arguments(lib):
     assert f(121, 8, good, good) == 3 and f(1, 2 ** 31 - 1, good, good) == 3
     assert f(0, 8, rows(0), good) == 1 and f(0, 8, good, rows(P, 2 * 8 * 64, 64, 7 * 64)) == 1
     assert B.ccgqa_launch_count() == 0
+
+
+def test_cache_attention_arguments(lib):
+    cfg, c = config(8, 2, 64), _cache(cap=4096)
+    ws = B.ccgqa_cache_attention_workspace_size(cfg, 3, 4096)
+    assert ws > 0 and B.ccgqa_cache_attention_workspace_size(cfg, 0, 64) == 0
+    assert B.ccgqa_cache_attention_workspace_size(config(8, 3, 64), 3, 64) == 0
+    f = lambda q=P, o=P, w=P, n=ws, win=None, cc=c, cf=cfg, c8=None: lib.ccgqa_cache_attention(  # noqa: E731
+        ctypes.byref(cf), None if win is None else ctypes.byref(B.ccgqa_window(*win)), ctypes.byref(cc),
+        None if c8 is None else ctypes.byref(c8), q, o, w, n, None, None)
+    assert f(q=None) == 1 and f(q=P + 8) == 1 and f(o=None) == 1 and f(o=P + 2) == 1
+    assert f(win=(-1, 0)) == 1 and f(win=(4, -1)) == 1
+    assert f(w=None) == 4 and f(w=P + 8) == 4 and f(n=ws - 1) == 4
+    assert f(c8=B.ccgqa_cache8(1, 24, P, P)) == 1
+    assert f(cf=config(8, 3, 64)) == 1
+    assert B.ccgqa_launch_count() == 0
+
+
+def test_cache_attention_workspace_fits_every_window(lib):
+    """The size for a cache is enough whatever the window (the same plan, fewer keys)."""
+    for geo in (config(8, 2, 64), config(48, 1, 128), config(8, 8, 16, "f32")):
+        for batch in (1, 3, 200):
+            sizes = [B.ccgqa_cache_attention_workspace_size(geo, batch, cap) for cap in (1, 64, 511, 513, 4096, 100000)]
+            assert sizes == sorted(sizes)
