@@ -131,6 +131,18 @@ def load() -> ctypes.CDLL:
                                           P(ccgqa_cache8), c_void_p, c_void_p, c_void_p, c_size_t,
                                           c_void_p, c_void_p]
     lib.ccgqa_cache_attention.restype = c_int
+    R = P(ccgqa_rows)
+    lib.ccgqa_window_attention_stats_size.argtypes = [P(ccgqa_config), c_int32, c_int32]
+    lib.ccgqa_window_attention_stats_size.restype = c_size_t
+    lib.ccgqa_window_attention.argtypes = [P(ccgqa_config), P(ccgqa_window), R, R, R, c_int32, c_int32,
+                                           R, c_void_p, c_void_p, c_void_p]
+    lib.ccgqa_window_attention.restype = c_int
+    lib.ccgqa_window_attention_backward_workspace_size.argtypes = [P(ccgqa_config), c_int32, c_int32]
+    lib.ccgqa_window_attention_backward_workspace_size.restype = c_size_t
+    lib.ccgqa_window_attention_backward.argtypes = [P(ccgqa_config), P(ccgqa_window), R, R, R, R, c_void_p,
+                                                    R, c_int32, c_int32, R, R, R, c_void_p, c_size_t,
+                                                    c_void_p, c_void_p]
+    lib.ccgqa_window_attention_backward.restype = c_int
     lib.ccgqa_status_string.argtypes = [c_int]
     lib.ccgqa_status_string.restype = c_char_p
     lib.ccgqa_launch_count.argtypes = []
@@ -355,6 +367,36 @@ def ccgqa_cache_attention(cfg, window, cache, cache8, q, out, workspace, dev_err
                                       _ptr(dev_err), _stream(stream))
     if check and st != 0:
         raise CCGQAError(st, "ccgqa_cache_attention")
+    return st
+
+
+def ccgqa_window_attention_stats_size(cfg: ccgqa_config, batch: int, seq_len: int) -> int:
+    return int(load().ccgqa_window_attention_stats_size(ctypes.byref(cfg), batch, seq_len))
+
+
+def ccgqa_window_attention(cfg, window, q, k, v, batch, seq_len, out, stats=None, dev_err=None,
+                           stream=None, check=True) -> int:
+    """q, k, v, out: ccgqa_rows (make_rows)."""
+    st = load().ccgqa_window_attention(ctypes.byref(cfg), _ref(window), _ref(q), _ref(k), _ref(v), batch,
+                                       seq_len, _ref(out), _ptr(stats), _ptr(dev_err), _stream(stream))
+    if check and st != 0:
+        raise CCGQAError(st, "ccgqa_window_attention")
+    return st
+
+
+def ccgqa_window_attention_backward_workspace_size(cfg: ccgqa_config, batch: int, seq_len: int) -> int:
+    return int(load().ccgqa_window_attention_backward_workspace_size(ctypes.byref(cfg), batch, seq_len))
+
+
+def ccgqa_window_attention_backward(cfg, window, q, k, v, out, stats, dout, batch, seq_len, dq, dk, dv,
+                                    workspace, dev_err=None, stream=None, check=True) -> int:
+    st = load().ccgqa_window_attention_backward(
+        ctypes.byref(cfg), _ref(window), _ref(q), _ref(k), _ref(v), _ref(out), _ptr(stats), _ref(dout),
+        batch, seq_len, _ref(dq), _ref(dk), _ref(dv), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(dev_err),
+        _stream(stream))
+    if check and st != 0:
+        raise CCGQAError(st, "ccgqa_window_attention_backward")
     return st
 
 

@@ -1,6 +1,6 @@
 // C ABI of the operators on finished query / key / value rows: the append with
-// the rotation, the cache read-back and the one-token attention over the cache.
-// Host-side validation and dispatch, as in api.cu: nothing is launched on a bad
+// the rotation, the cache read-back, the one-token attention over the cache and
+// the window attention of whole sequences with its gradients.  Host-side validation and dispatch, as in api.cu: nothing is launched on a bad
 // argument.
 #include <algorithm>
 
@@ -96,6 +96,43 @@ size_t attn_workspace(const Geo& g, int64_t batch, int splits) {
   const int64_t rows = attn_units(g, batch) * splits * (g.dtype == CCGQA_BF16 ? kCacheAttnHeads : kCacheAttnHeadsF32);
   return static_cast<size_t>(rows) * (g.d + 2) * sizeof(float);
 }
+// Rows of softmax statistics per (sequence, kv head): see WindowArgs.
+int64_t stat_rows(const Geo& g, int64_t S) {
+  if (g.G > 64) return (S * g.G + 63) / 64 * 64;
+  const int64_t pos = 64 / g.G;
+  return (S + pos - 1) / pos * 64;
+}
+// The fields both directions share; false when a tensor does not fit.
+bool window_args(const Geo& g, const ccgqa_window* win, int B, int S, const ccgqa_rows* q,
+                 const ccgqa_rows* k, const ccgqa_rows* v, const ccgqa_rows* out, int32_t* dev_err,
+                 WindowArgs* a) {
+  if (!q || !k || !v || !out) return false;
+  if (!rows_ok(g, *q, B, S, g.Hq) || !rows_ok(g, *k, B, S, g.Hkv) || !rows_ok(g, *v, B, S, g.Hkv) ||
+      !rows_ok(g, *out, B, S, g.Hq))
+    return false;
+  *a = WindowArgs{};
+  a->B = B;
+  a->S = S;
+  a->Hq = g.Hq;
+  a->Hkv = g.Hkv;
+  a->d = g.d;
+  a->G = g.G;
+  a->window = win && win->window > 0 ? std::min(win->window, S) : S;
+  a->sinks = win && win->window > 0 ? std::min(win->sinks, S) : 0;
+  a->q = rows_of(*q, B, S, g.Hq);
+  a->k = rows_of(*k, B, S, g.Hkv);
+  a->v = rows_of(*v, B, S, g.Hkv);
+  a->out = rows_of(*out, B, S, g.Hq);
+  a->ld = stat_rows(g, S);
+  a->pos = g.G <= 64 ? 64 / g.G : 0;
+  a->dev_err = dev_err;
+  return true;
+}
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255) == 0; }
+size_t window_bwd_workspace(const Geo& g, int64_t B, int64_t S) {
+  return static_cast<size_t>(B * g.Hkv * stat_rows(g, S)) * sizeof(float);
+}
+
 bool window_ok(const ccgqa_window* w) { return !w || (w->window >= 0 && w->sinks >= 0); }
 
 }  // namespace
@@ -225,5 +262,72 @@ CCGQA_API ccgqa_status ccgqa_cache_attention(const ccgqa_config* cfg, const ccgq
   const int fmt = c8 ? c8->format : 0;
   const cudaError_t e = g.dtype == CCGQA_BF16 ? launch_cache_attn<bf16>(a, fmt, st)
                                               : launch_cache_attn<float>(a, fmt, st);
+  return e == cudaSuccess ? CCGQA_OK : cuda_fail(e);
+}
+
+CCGQA_API size_t ccgqa_window_attention_stats_size(const ccgqa_config* cfg, int32_t batch,
+                                                   int32_t seq_len) {
+  Geo g;
+  if (derive(cfg, &g) != CCGQA_OK || batch <= 0 || seq_len <= 0) return 0;
+  return static_cast<size_t>(static_cast<int64_t>(batch) * g.Hkv * stat_rows(g, seq_len));
+}
+
+CCGQA_API ccgqa_status ccgqa_window_attention(const ccgqa_config* cfg, const ccgqa_window* win,
+                                              const ccgqa_rows* q, const ccgqa_rows* k,
+                                              const ccgqa_rows* v, int32_t batch, int32_t seq_len,
+                                              const ccgqa_rows* out, float* stats,
+                                              int32_t* dev_err, void* stream) {
+  Geo g;
+  const ccgqa_status s = derive(cfg, &g);
+  if (s != CCGQA_OK) return s;
+  if (!g.causal) return CCGQA_ERR_UNSUPPORTED;
+  if (!window_ok(win) || batch < 0 || seq_len < 0 || !aligned256(stats)) return CCGQA_ERR_INVALID_ARG;
+  if (batch == 0 || seq_len == 0) return CCGQA_OK;
+  WindowArgs a;
+  if (!window_args(g, win, batch, seq_len, q, k, v, out, dev_err, &a)) return CCGQA_ERR_INVALID_ARG;
+  a.stats = stats;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!stream_allowed(st)) return CCGQA_ERR_INVALID_ARG;
+  const cudaError_t e = g.dtype == CCGQA_BF16 ? launch_window_simt<bf16>(a, st) : launch_window_simt<float>(a, st);
+  return e == cudaSuccess ? CCGQA_OK : cuda_fail(e);
+}
+
+CCGQA_API size_t ccgqa_window_attention_backward_workspace_size(const ccgqa_config* cfg,
+                                                                int32_t batch, int32_t seq_len) {
+  Geo g;
+  if (derive(cfg, &g) != CCGQA_OK || batch <= 0 || seq_len <= 0) return 0;
+  return window_bwd_workspace(g, batch, seq_len);
+}
+
+CCGQA_API ccgqa_status ccgqa_window_attention_backward(
+    const ccgqa_config* cfg, const ccgqa_window* win, const ccgqa_rows* q, const ccgqa_rows* k,
+    const ccgqa_rows* v, const ccgqa_rows* out, const float* stats, const ccgqa_rows* dout,
+    int32_t batch, int32_t seq_len, const ccgqa_rows* dq, const ccgqa_rows* dk,
+    const ccgqa_rows* dv, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+    void* stream) {
+  Geo g;
+  const ccgqa_status s = derive(cfg, &g);
+  if (s != CCGQA_OK) return s;
+  if (!g.causal) return CCGQA_ERR_UNSUPPORTED;
+  if (!window_ok(win) || batch < 0 || seq_len < 0) return CCGQA_ERR_INVALID_ARG;
+  if (batch == 0 || seq_len == 0) return CCGQA_OK;
+  WindowArgs a;
+  if (!window_args(g, win, batch, seq_len, q, k, v, out, dev_err, &a)) return CCGQA_ERR_INVALID_ARG;
+  if (!stats || !aligned256(stats) || !dout || !dq || !dk || !dv) return CCGQA_ERR_INVALID_ARG;
+  if (!rows_ok(g, *dout, batch, seq_len, g.Hq) || !rows_ok(g, *dq, batch, seq_len, g.Hq) ||
+      !rows_ok(g, *dk, batch, seq_len, g.Hkv) || !rows_ok(g, *dv, batch, seq_len, g.Hkv))
+    return CCGQA_ERR_INVALID_ARG;
+  if (!workspace || !aligned256(workspace) || workspace_bytes < window_bwd_workspace(g, batch, seq_len))
+    return CCGQA_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!stream_allowed(st)) return CCGQA_ERR_INVALID_ARG;
+  a.stats = const_cast<float*>(stats);
+  a.dsum = static_cast<float*>(workspace);
+  a.dout = rows_of(*dout, batch, seq_len, g.Hq);
+  a.dq = rows_of(*dq, batch, seq_len, g.Hq);
+  a.dk = rows_of(*dk, batch, seq_len, g.Hkv);
+  a.dv = rows_of(*dv, batch, seq_len, g.Hkv);
+  const cudaError_t e =
+      g.dtype == CCGQA_BF16 ? launch_window_bwd_simt<bf16>(a, st) : launch_window_bwd_simt<float>(a, st);
   return e == cudaSuccess ? CCGQA_OK : cuda_fail(e);
 }

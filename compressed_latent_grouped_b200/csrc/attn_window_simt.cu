@@ -1,0 +1,390 @@
+// Causal grouped-query attention of whole sequences over a sliding window with
+// sink tokens, and its gradients, on the CUDA cores: the fp32 path (operands
+// are not rounded to a tensor-core type) and bf16 where the tensor-core kernels
+// do not apply.  ("Compressed Convolutional Attention", CCGQA; the window
+// bounds the keys a query reads, the sinks keep the first tokens in sight.)
+//
+// Query t sees key s when s <= t and (s > t - window or s < sinks).
+//   o = sum_s p_s v_s,  p_s = 2^(c q.k_s - lse),  c = log2(e) / sqrt(d)
+//   D = dO.o,  dS = p (dO.v - D),  dq = dS k / sqrt(d),  dk = dS^T q / sqrt(d),
+//   dv = p^T dO, the last two summed over the heads of a group.
+//
+// Tiles of 64 queries by 64 keys, 256 threads, each 4 x 4 scores: operands in
+// shared memory as fp32 rows padded by 16 bytes, so that 8 neighbouring rows'
+// 16-byte reads fall into different banks; 64 fused multiply-adds per 8 reads of
+// 16 bytes.  Only tiles with a visible pair are visited.  The bound is the FMA
+// pipe.  dk and dv of a key tile belong to one CTA, which walks the group's
+// heads and the query tiles that see it, so nothing is added by atomics and
+// equal calls give equal bits.
+#include "kernels.h"
+
+namespace ccgqa {
+namespace {
+
+constexpr int kT = 64, kThreads = 256, kPs = kT + 4;
+constexpr float kLog2eW = 1.4426950408889634f;
+
+template <int D>
+struct SimtCfg {
+  static constexpr int kLd = D + 4;             // floats of a padded row
+  static constexpr int kCols = D / 16;          // output columns of a thread
+  static constexpr int kVec = kCols < 4 ? kCols : 4;
+  static constexpr size_t kTileBytes = sizeof(float) * kT * kLd;
+  static constexpr size_t kPBytes = sizeof(float) * kT * kPs;
+  // output column n of thread tx
+  __device__ static __forceinline__ int col(int tx, int n) {
+    return (n / kVec) * 16 * kVec + tx * kVec + n % kVec;
+  }
+};
+
+template <int N>
+__device__ __forceinline__ void load_n(const float* p, float (&x)[N]) {
+  if constexpr (N == 1) {
+    x[0] = *p;
+  } else if constexpr (N == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x;
+    x[1] = v.y;
+  } else {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = v.x;
+    x[1] = v.y;
+    x[2] = v.z;
+    x[3] = v.w;
+  }
+}
+
+// Rows [t0, t0 + 64) of a head into shared memory as fp32; zeros past S.
+template <typename T, int D>
+__device__ __forceinline__ void load_tile(float* dst, const Rows& r, int b, int t0, int h, int S) {
+  constexpr int V = 16 / sizeof(T), N = D / V;
+  const T* base = static_cast<const T*>(r.ptr) + b * r.batch + h * r.head;
+  for (int x = threadIdx.x; x < kT * N; x += kThreads) {
+    const int row = x / N, u = x % N, t = t0 + row;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (t < S) w = *reinterpret_cast<const uint4*>(base + t * r.token + u * V);
+    const T* e = reinterpret_cast<const T*>(&w);
+    float* d = dst + row * SimtCfg<D>::kLd + u * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = to_f32(e[i]);
+  }
+}
+
+// s[i][j] += a[ty 4 + i] . b[tx + 16 j]
+template <int D>
+__device__ __forceinline__ void dot_tile(const float* a, const float* b, int ty, int tx, float (&s)[4][4]) {
+  constexpr int L = SimtCfg<D>::kLd;
+#pragma unroll 4
+  for (int e = 0; e < D; e += 4) {
+    float x[4][4], y[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_n<4>(a + (ty * 4 + i) * L + e, x[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_n<4>(b + (tx + 16 * j) * L + e, y[j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[i][j] = fmaf(x[i][u], y[j][u], s[i][j]);
+  }
+}
+
+// o[i][n] += sum_k w[ty 4 + i][k] b[k][col n]   (kTrans: w[k][ty 4 + i])
+template <int D, bool kTrans>
+__device__ __forceinline__ void mix_tile(const float* w, const float* b, int ty, int tx,
+                                         float (&o)[4][SimtCfg<D>::kCols]) {
+  using C = SimtCfg<D>;
+#pragma unroll 2
+  for (int k = 0; k < kT; k += 4) {
+    float x[4][4];   // kTrans: [k][i], else [i][k]
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      load_n<4>(kTrans ? w + (k + i) * kPs + ty * 4 : w + (ty * 4 + i) * kPs + k, x[i]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int n = 0; n < C::kCols; n += C::kVec) {
+        float y[C::kVec];
+        load_n<C::kVec>(b + (k + u) * C::kLd + C::col(tx, n), y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int v = 0; v < C::kVec; ++v)
+            o[i][n + v] = fmaf(kTrans ? x[u][i] : x[i][u], y[v], o[i][n + v]);
+      }
+  }
+}
+
+__device__ __forceinline__ bool sees(int t, int s, int window, int sinks) {
+  return s <= t && (s > t - window || s < sinks);
+}
+
+// Key tiles that queries [t0, t0 + 64) see: the sinks' tiles, then the window's.
+struct KeyTiles {
+  int n_sink, first, n;
+  __device__ __forceinline__ KeyTiles(int t0, int S, int window, int sinks) {
+    const int lo = max(0, t0 - window + 1), last = min(t0 + kT, S) - 1;
+    first = lo / kT;
+    n_sink = min((min(sinks, lo) + kT - 1) / kT, first);
+    n = n_sink + last / kT - first + 1;
+  }
+  __device__ __forceinline__ int start(int i) const { return (i < n_sink ? i : first + i - n_sink) * kT; }
+};
+
+template <typename T, int D>
+__device__ __forceinline__ void store_rows(const Rows& r, int b, int t0, int h, int S, int ty, int tx,
+                                           const float (&o)[4][SimtCfg<D>::kCols], const float (&f)[4]) {
+  using C = SimtCfg<D>;
+  T* base = static_cast<T*>(r.ptr) + b * r.batch + h * r.head;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + ty * 4 + i;
+    if (t >= S) continue;
+#pragma unroll
+    for (int n = 0; n < C::kCols; ++n) base[t * r.token + C::col(tx, n)] = from_f32<T>(o[i][n] * f[i]);
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+    window_fwd_simt_kernel(const __grid_constant__ WindowArgs a) {
+  pdl_enter();
+  using C = SimtCfg<D>;
+  extern __shared__ __align__(16) float sm[];
+  float *Q = sm, *K = Q + kT * C::kLd, *V = K + kT * C::kLd, *P = V + kT * C::kLd;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int tiles = (a.S + kT - 1) / kT;
+  const int t0 = (tiles - 1 - static_cast<int>(blockIdx.x) % tiles) * kT;
+  const int h = static_cast<int>(blockIdx.x) / tiles % a.Hq, b = static_cast<int>(blockIdx.x) / tiles / a.Hq;
+  const int g = h / a.G;
+  load_tile<T, D>(Q, a.q, b, t0, h, a.S);
+  const KeyTiles kt(t0, a.S, a.window, a.sinks);
+  float o[4][C::kCols], m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int n = 0; n < C::kCols; ++n) o[i][n] = 0.f;
+  }
+  const float c = kLog2eW * rsqrtf(static_cast<float>(D));
+  for (int it = 0; it < kt.n; ++it) {
+    const int s0 = kt.start(it);
+    __syncthreads();
+    load_tile<T, D>(K, a.k, b, s0, g, a.S);
+    load_tile<T, D>(V, a.v, b, s0, g, a.S);
+    __syncthreads();
+    float s[4][4] = {};
+    dot_tile<D>(Q, K, ty, tx, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + ty * 4 + i;
+      float top = m[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = sees(t, s0 + tx + 16 * j, a.window, a.sinks) ? s[i][j] * c : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      const float base = top == -INFINITY ? 0.f : top;
+      const float f = m[i] == -INFINITY ? 1.f : exp2f(m[i] - base);
+      m[i] = top;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(s[i][j] - base);
+        sum += p;
+        P[(ty * 4 + i) * kPs + tx + 16 * j] = p;
+      }
+      l[i] = l[i] * f + sum;   // of this thread's columns; joined at the end
+#pragma unroll
+      for (int n = 0; n < C::kCols; ++n) o[i][n] *= f;
+    }
+    __syncwarp();   // a row of P is written and read by one half warp
+    mix_tile<D, false>(P, V, ty, tx, o);
+  }
+  float f[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+    f[i] = 1.f / l[i];
+    const int t = t0 + ty * 4 + i;
+    if (a.stats && t < a.S && tx == 0) a.stats[a.stat_row(b * a.Hkv + g, t, h - g * a.G)] = -(m[i] + log2f(l[i]));
+  }
+  store_rows<T, D>(a.out, b, t0, h, a.S, ty, tx, o, f);
+}
+
+// p and dS of a tile, into shared memory.  L, Ds: -lse and -D of this thread's rows.
+template <int D>
+__device__ __forceinline__ void score_grads(const WindowArgs& a, const float* Q, const float* dO, const float* K,
+                                            const float* V, float* P, float* dS, int t0, int s0, int ty, int tx,
+                                            const float (&L)[4], const float (&Ds)[4], float c) {
+  float s[4][4] = {}, e[4][4] = {};
+  dot_tile<D>(Q, K, ty, tx, s);
+  dot_tile<D>(dO, V, ty, tx, e);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + ty * 4 + i;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = s0 + tx + 16 * j;
+      const float p = t < a.S && sees(t, k, a.window, a.sinks) ? exp2f(fmaf(s[i][j], c, L[i])) : 0.f;
+      if (P) P[(ty * 4 + i) * kPs + tx + 16 * j] = p;
+      dS[(ty * 4 + i) * kPs + tx + 16 * j] = p == 0.f ? 0.f : p * (e[i][j] + Ds[i]);
+    }
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+    window_dq_simt_kernel(const __grid_constant__ WindowArgs a) {
+  pdl_enter();
+  using C = SimtCfg<D>;
+  extern __shared__ __align__(16) float sm[];
+  float *Q = sm, *dO = Q + kT * C::kLd, *K = dO + kT * C::kLd, *V = K + kT * C::kLd, *dS = V + kT * C::kLd;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int tiles = (a.S + kT - 1) / kT;
+  const int t0 = (tiles - 1 - static_cast<int>(blockIdx.x) % tiles) * kT;
+  const int h = static_cast<int>(blockIdx.x) / tiles % a.Hq, b = static_cast<int>(blockIdx.x) / tiles / a.Hq;
+  const int g = h / a.G;
+  load_tile<T, D>(Q, a.q, b, t0, h, a.S);
+  load_tile<T, D>(dO, a.dout, b, t0, h, a.S);
+  load_tile<T, D>(K, a.out, b, t0, h, a.S);   // o, for D
+  __syncthreads();
+  float L[4], Ds[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = ty * 4 + i, t = t0 + row;
+    float x = 0.f;
+    for (int e = tx; e < D; e += 16) x = fmaf(dO[row * C::kLd + e], K[row * C::kLd + e], x);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    Ds[i] = -x;
+    L[i] = 0.f;
+    if (t < a.S) {
+      const int64_t at = a.stat_row(b * a.Hkv + g, t, h - g * a.G);
+      L[i] = a.stats[at];
+      if (tx == 0) a.dsum[at] = -x;
+    }
+  }
+  const KeyTiles kt(t0, a.S, a.window, a.sinks);
+  float o[4][C::kCols] = {};
+  const float c = kLog2eW * rsqrtf(static_cast<float>(D));
+  for (int it = 0; it < kt.n; ++it) {
+    const int s0 = kt.start(it);
+    __syncthreads();
+    load_tile<T, D>(K, a.k, b, s0, g, a.S);
+    load_tile<T, D>(V, a.v, b, s0, g, a.S);
+    __syncthreads();
+    score_grads<D>(a, Q, dO, K, V, nullptr, dS, t0, s0, ty, tx, L, Ds, c);
+    __syncwarp();
+    mix_tile<D, false>(dS, K, ty, tx, o);
+  }
+  const float inv = rsqrtf(static_cast<float>(D));
+  const float f[4] = {inv, inv, inv, inv};
+  store_rows<T, D>(a.dq, b, t0, h, a.S, ty, tx, o, f);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+    window_dkv_simt_kernel(const __grid_constant__ WindowArgs a) {
+  pdl_enter();
+  using C = SimtCfg<D>;
+  extern __shared__ __align__(16) float sm[];
+  float *Q = sm, *dO = Q + kT * C::kLd, *K = dO + kT * C::kLd, *V = K + kT * C::kLd;
+  float *P = V + kT * C::kLd, *dS = P + kT * kPs;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int tiles = (a.S + kT - 1) / kT;
+  const int s0 = static_cast<int>(blockIdx.x) % tiles * kT;   // the sinks' tile, the longest, starts first
+  const int g = static_cast<int>(blockIdx.x) / tiles % a.Hkv, b = static_cast<int>(blockIdx.x) / tiles / a.Hkv;
+  load_tile<T, D>(K, a.k, b, s0, g, a.S);
+  load_tile<T, D>(V, a.v, b, s0, g, a.S);
+  // queries up to t_end see a key of the tile
+  const int64_t reach = static_cast<int64_t>(s0) + kT - 1 + a.window;
+  const int t_end = s0 < a.sinks || reach > a.S ? a.S : static_cast<int>(reach);
+  float dk[4][C::kCols] = {}, dv[4][C::kCols] = {};
+  const float c = kLog2eW * rsqrtf(static_cast<float>(D));
+  for (int hl = 0; hl < a.G; ++hl) {
+    const int h = g * a.G + hl;
+    for (int t0 = s0; t0 < t_end; t0 += kT) {
+      __syncthreads();
+      load_tile<T, D>(Q, a.q, b, t0, h, a.S);
+      load_tile<T, D>(dO, a.dout, b, t0, h, a.S);
+      float L[4], Ds[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = t0 + ty * 4 + i;
+        const int64_t at = a.stat_row(b * a.Hkv + g, min(t, a.S - 1), hl);
+        L[i] = a.stats[at];
+        Ds[i] = a.dsum[at];
+      }
+      __syncthreads();
+      score_grads<D>(a, Q, dO, K, V, P, dS, t0, s0, ty, tx, L, Ds, c);
+      __syncthreads();
+      mix_tile<D, true>(P, dO, ty, tx, dv);
+      mix_tile<D, true>(dS, Q, ty, tx, dk);
+    }
+  }
+  const float inv = rsqrtf(static_cast<float>(D));
+  const float fk[4] = {inv, inv, inv, inv}, fv[4] = {1.f, 1.f, 1.f, 1.f};
+  store_rows<T, D>(a.dk, b, s0, g, a.S, ty, tx, dk, fk);
+  store_rows<T, D>(a.dv, b, s0, g, a.S, ty, tx, dv, fv);
+}
+
+template <typename Kernel>
+cudaError_t launch_one(Kernel* kernel, int64_t grid, size_t smem, const WindowArgs& a, cudaStream_t stream) {
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, stream, a);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t fwd_d(const WindowArgs& a, cudaStream_t stream) {
+  using C = SimtCfg<D>;
+  return launch_one(window_fwd_simt_kernel<T, D>, static_cast<int64_t>((a.S + kT - 1) / kT) * a.Hq * a.B,
+                    3 * C::kTileBytes + C::kPBytes, a, stream);
+}
+template <typename T, int D>
+cudaError_t bwd_d(const WindowArgs& a, cudaStream_t stream) {
+  using C = SimtCfg<D>;
+  const int64_t tiles = (a.S + kT - 1) / kT;
+  const cudaError_t e = launch_one(window_dq_simt_kernel<T, D>, tiles * a.Hq * a.B, 4 * C::kTileBytes + C::kPBytes, a, stream);
+  if (e != cudaSuccess) return e;
+  return launch_one(window_dkv_simt_kernel<T, D>, tiles * a.Hkv * a.B, 4 * C::kTileBytes + 2 * C::kPBytes, a, stream);
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t launch_window_simt(const WindowArgs& a, cudaStream_t stream) {
+  switch (a.d) {
+    case 16: return fwd_d<T, 16>(a, stream);
+    case 32: return fwd_d<T, 32>(a, stream);
+    case 64: return fwd_d<T, 64>(a, stream);
+    case 128: return fwd_d<T, 128>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+template <typename T>
+cudaError_t launch_window_bwd_simt(const WindowArgs& a, cudaStream_t stream) {
+  switch (a.d) {
+    case 16: return bwd_d<T, 16>(a, stream);
+    case 32: return bwd_d<T, 32>(a, stream);
+    case 64: return bwd_d<T, 64>(a, stream);
+    case 128: return bwd_d<T, 128>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+template cudaError_t launch_window_simt<float>(const WindowArgs&, cudaStream_t);
+template cudaError_t launch_window_simt<bf16>(const WindowArgs&, cudaStream_t);
+template cudaError_t launch_window_bwd_simt<float>(const WindowArgs&, cudaStream_t);
+template cudaError_t launch_window_bwd_simt<bf16>(const WindowArgs&, cudaStream_t);
+
+}  // namespace ccgqa

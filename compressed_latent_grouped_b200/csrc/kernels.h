@@ -289,6 +289,31 @@ int cache_attn_splits(int64_t units, int64_t keys);
 template <typename T>
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int fmt, cudaStream_t stream);
 
+// Attention of whole sequences over a sliding window with sinks
+// (ccgqa_window_attention and its backward).
+struct WindowArgs {
+  int B, S, Hq, Hkv, d, G;
+  int window, sinks;            // at most S; window = S: the whole prefix
+  Rows q, k, v, out;
+  // -log2(sum_s 2^(log2(e) q.k_s / sqrt(d))) and -rowsum(dO o) per query row,
+  // in groups of 64: pos = 64 / G positions with their G heads (G <= 64), else
+  // (pos = 0) t G + head; ld rows per (sequence, kv head)
+  float* stats;                 // forward: nullable
+  float* dsum;
+  int64_t ld;
+  int pos;
+  // backward
+  Rows dout, dq, dk, dv;
+  int32_t* dev_err;
+  __device__ __forceinline__ int64_t stat_row(int bg, int t, int hl) const {
+    return bg * ld + (pos ? static_cast<int64_t>(t / pos) * 64 + t % pos * G : static_cast<int64_t>(t) * G) + hl;
+  }
+};
+template <typename T>
+cudaError_t launch_window_simt(const WindowArgs& a, cudaStream_t stream);
+template <typename T>
+cudaError_t launch_window_bwd_simt(const WindowArgs& a, cudaStream_t stream);
+
 // Split plan for the decode step, shared by the workspace-size query and the launch.
 void decode_plan(int B, int Hkv, int E, int N, int64_t cap, bool has_proj, int es,
                  int* e_splits, int* splits, int* chunk);

@@ -343,6 +343,64 @@ class DeviceKVCache:
         return int(self.dev_err.item())
 
 
+def _window_inputs(where, cfg, q, k, v):
+    if q.dim() != 4:
+        _bad(where, "q is not 4-dimensional")
+    batch, S = q.shape[:2]
+    dt, d = _dtype_of(cfg), head_dim(cfg)
+    if q.device.type != "cuda":
+        raise RuntimeError("CCGQA needs a CUDA device")
+    q_shape, kv_shape = (batch, S, cfg.n_q_heads, d), (batch, S, cfg.n_kv_heads, d)
+    _check(where, "q", q, q_shape, dt, q.device)
+    _check(where, "k", k, kv_shape, dt, q.device)
+    _check(where, "v", v, kv_shape, dt, q.device)
+    return batch, S, dt, q.device, q_shape, kv_shape
+
+
+def window_attention(cfg, q, k, v, window: int = 0, sinks: int = 0, out=None, with_stats: bool = False,
+                     dev_err=None, stream=None):
+    """Causal attention of whole sequences, q [batch, S, Hq, d], k and v [batch,
+    S, Hkv, d] (any strides between the heads' rows): every query sees its last
+    ``window`` keys and the first ``sinks`` (window 0: all before it).  Returns
+    out, or with ``with_stats`` (out, stats), which the backward pass takes."""
+    where = "window_attention"
+    batch, S, dt, dev, q_shape, _ = _window_inputs(where, cfg, q, k, v)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty(q_shape, dtype=dt, device=dev)
+        _check(where, "out", out, q_shape, dt, dev)
+        stats = None
+        if with_stats:
+            stats = torch.empty(B.ccgqa_window_attention_stats_size(cfg, batch, S), dtype=torch.float32, device=dev)
+        rows = B.make_rows
+        B.ccgqa_window_attention(cfg, B.ccgqa_window(window, sinks), rows(q), rows(k), rows(v), batch, S, rows(out),
+                                 stats, dev_err, stream)
+    return (out, stats) if with_stats else out
+
+
+def window_attention_backward(cfg, q, k, v, out, stats, dout, window: int = 0, sinks: int = 0, dq=None,
+                              dk=None, dv=None, dev_err=None, stream=None):
+    """Gradients (dq, dk, dv) of ``window_attention`` for the gradient ``dout``
+    of its output; ``out`` and ``stats`` are what it returned."""
+    where = "window_attention_backward"
+    batch, S, dt, dev, q_shape, kv_shape = _window_inputs(where, cfg, q, k, v)
+    _check(where, "out", out, q_shape, dt, dev)
+    _check(where, "dout", dout, q_shape, dt, dev)
+    _check_dense(where, "stats", stats, (B.ccgqa_window_attention_stats_size(cfg, batch, S),), torch.float32, dev)
+    with torch.cuda.device(dev):
+        dq, dk, dv = (torch.empty(shape, dtype=dt, device=dev) if x is None else x
+                      for x, shape in ((dq, q_shape), (dk, kv_shape), (dv, kv_shape)))
+        _check(where, "dq", dq, q_shape, dt, dev)
+        _check(where, "dk", dk, kv_shape, dt, dev)
+        _check(where, "dv", dv, kv_shape, dt, dev)
+        ws = _workspace(B.ccgqa_window_attention_backward_workspace_size(cfg, batch, S), dev, stream)
+        rows = B.make_rows
+        B.ccgqa_window_attention_backward(cfg, B.ccgqa_window(window, sinks), rows(q), rows(k), rows(v), rows(out),
+                                          stats, rows(dout), batch, S, rows(dq), rows(dk), rows(dv), ws, dev_err,
+                                          stream)
+    return dq, dk, dv
+
+
 class Graph:
     """Library calls recorded once into a CUDA graph (ccgqa_graph_*) and
     launched again with the same arguments: ``Graph(fn, stream)`` records what

@@ -310,11 +310,12 @@ CCGQA_API ccgqa_status ccgqa_output_projection(const ccgqa_config* cfg, const vo
                                                int32_t* dev_err, void* stream);
 
 /* ---------------------------------------------------------------------------
- * Cache operators on rows that are already queries, keys and values (a plain
+ * Operators on rows that are already queries, keys and values (a plain
  * grouped-query layer, or one that makes its own rows): the append with the
- * rotation and the one-token attention over the cache.
+ * rotation, the one-token attention over the cache, and the attention of whole
+ * sequences over a sliding window with its gradients.
  * Of cfg they use E, C, n_q_heads, n_kv_heads (head dim d = E / (C Hq)), dtype
- * and, where stated, rope_base; cfg is validated as for every call.
+ * and, where stated, rope_base and causal; cfg is validated as for every call.
  * ------------------------------------------------------------------------- */
 
 /* A tensor of head rows [batch, tokens, heads, d]: element (b, t, h, e) lies at
@@ -426,6 +427,47 @@ CCGQA_API ccgqa_status ccgqa_cache_attention(const ccgqa_config* cfg, const ccgq
                                              const void* q, void* out, void* workspace,
                                              size_t workspace_bytes, int32_t* dev_err,
                                              void* stream);
+
+/* Floats of the softmax statistics ccgqa_window_attention can keep for its
+ * backward pass (0 on an invalid configuration); the layout is the library's. */
+CCGQA_API size_t ccgqa_window_attention_stats_size(const ccgqa_config* cfg, int32_t batch,
+                                                   int32_t seq_len);
+
+/* Causal grouped-query attention of whole sequences over a window with sinks:
+ *   out[b, t, h] = sum_s softmax_s(q[b, t, h] . k[b, s, h / G] / sqrt(d)) v[b, s, h / G]
+ * over the keys s that query t sees (ccgqa_window).
+ *  - q, out: [batch, seq_len, Hq, d]; k, v: [batch, seq_len, Hkv, d]; out must
+ *    not overlap q, k or v.  cfg->causal must be 1 (CCGQA_ERR_UNSUPPORTED);
+ *    rope_base is not used (rotate q and k first).
+ *  - stats: nullable, ccgqa_window_attention_stats_size floats, 256-byte
+ *    aligned; needed by the backward pass.
+ *  - Only key tiles that a query tile sees are visited: work and time grow
+ *    with seq_len * (window + sinks).  CUDA cores, fp32 throughout.
+ *  - k and v must be finite: a key that is masked for a query has weight zero,
+ *    but zero times an infinity or NaN in its tile is NaN. */
+CCGQA_API ccgqa_status ccgqa_window_attention(const ccgqa_config* cfg, const ccgqa_window* win,
+                                              const ccgqa_rows* q, const ccgqa_rows* k,
+                                              const ccgqa_rows* v, int32_t batch, int32_t seq_len,
+                                              const ccgqa_rows* out, float* stats,
+                                              int32_t* dev_err, void* stream);
+
+/* Workspace bytes of ccgqa_window_attention_backward for any window (0 on an
+ * invalid configuration); 256-byte aligned, contents need no preparation. */
+CCGQA_API size_t ccgqa_window_attention_backward_workspace_size(const ccgqa_config* cfg,
+                                                                int32_t batch, int32_t seq_len);
+
+/* Gradients of ccgqa_window_attention: given q, k, v, its out and stats and the
+ * gradient dout of out, writes dq, dk, dv (shapes of q, k, v; a kv head's
+ * gradient is summed over its G query heads).  Sums in fp32, each gradient
+ * rounded once to cfg->dtype; the order of every sum is fixed, so equal
+ * calls give equal bits.  dq, dk, dv overlap neither each other nor an
+ * input. */
+CCGQA_API ccgqa_status ccgqa_window_attention_backward(
+    const ccgqa_config* cfg, const ccgqa_window* win, const ccgqa_rows* q, const ccgqa_rows* k,
+    const ccgqa_rows* v, const ccgqa_rows* out, const float* stats, const ccgqa_rows* dout,
+    int32_t batch, int32_t seq_len, const ccgqa_rows* dq, const ccgqa_rows* dk,
+    const ccgqa_rows* dv, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+    void* stream);
 
 /* Static description of a status code. */
 CCGQA_API const char* ccgqa_status_string(ccgqa_status s);

@@ -117,3 +117,49 @@ def test_cache_attention_workspace_fits_every_window(lib):
         for batch in (1, 3, 200):
             sizes = [B.ccgqa_cache_attention_workspace_size(geo, batch, cap) for cap in (1, 64, 511, 513, 4096, 100000)]
             assert sizes == sorted(sizes)
+
+
+def test_window_attention_arguments(lib):
+    cfg = config(8, 2, 64)
+    Q, K = (1 << 20, 512, 64), (1 << 20, 128, 64)
+    q, k = rows(P, *Q), rows(P, *K)
+    fwd = lambda cf=cfg, win=None, q=q, k=k, v=k, n=(2, 100), o=q, st=None: B.ccgqa_window_attention(  # noqa: E731
+        cf, None if win is None else B.ccgqa_window(*win), q, k, v, *n, o,
+        None if st is None else _At(st), stream=0, check=False)
+    assert fwd(q=rows(0, *Q)) == 1 and fwd(q=None) == 1 and fwd(v=rows(P + 8, *K)) == 1
+    assert fwd(k=rows(P, 1 << 20, 64, 64)) == 1          # the heads of neighbouring tokens overlap
+    assert fwd(o=rows(P, 1000, 512, 64)) == 1            # sequences overlap
+    assert fwd(win=(-1, 0)) == 1 and fwd(win=(1, -1)) == 1
+    assert fwd(n=(-1, 5)) == 1 and fwd(n=(1, -5)) == 1 and fwd(n=(0, 5)) == 0 and fwd(n=(5, 0)) == 0
+    assert fwd(st=P + 128) == 1                          # statistics not on 256 bytes
+    two_way = config(8, 2, 64)
+    two_way.causal = 0
+    assert fwd(cf=two_way) == 2
+    ws = B.ccgqa_window_attention_backward_workspace_size(cfg, 2, 100)
+    assert ws > 0 and B.ccgqa_window_attention_stats_size(cfg, 2, 100) >= 2 * 8 * 100
+    assert B.ccgqa_window_attention_backward_workspace_size(cfg, 0, 100) == 0
+    assert B.ccgqa_window_attention_stats_size(config(8, 3, 64), 2, 100) == 0
+
+    def bwd(st=P, do=q, dq=q, dk=k, dv=k, w=P, n=ws):
+        return B.ccgqa_window_attention_backward(cfg, None, q, k, k, q, _At(st), do, 2, 100, dq, dk, dv, _At(w, n),
+                                                 stream=0, check=False)
+    assert bwd(st=0) == 1 and bwd(st=P + 16) == 1 and bwd(do=rows(0, *Q)) == 1 and bwd(dk=None) == 1
+    assert bwd(dv=rows(P, 1 << 20, 128, 32)) == 1 and bwd(dq=rows(P + 2, *Q)) == 1
+    assert bwd(w=P + 16) == 4 and bwd(n=ws - 1) == 4 and bwd(w=0) == 4
+    assert B.ccgqa_launch_count() == 0
+
+
+class _At:
+    """A device tensor's address and size; never dereferenced."""
+
+    def __init__(self, addr, n=1 << 30):
+        self.addr, self.n = addr, n
+
+    def data_ptr(self):
+        return self.addr
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return 1
