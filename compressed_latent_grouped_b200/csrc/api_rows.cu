@@ -16,7 +16,7 @@ bool rows_ok(const Geo& g, const ccgqa_rows& r, int64_t batch, int64_t tokens, i
     int64_t stride, n;
   } d[3] = {{r.batch, batch}, {r.token, tokens}, {r.head, heads}};
   std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
-  constexpr int64_t kMax = int64_t(1) << 39;   // keeps every product below in range
+  constexpr int64_t kMax = int64_t(1) << 38;   // in bytes within a TMA stride; every product below in range
   int64_t extent = g.d;
   for (const Dim& x : d) {
     if (x.n <= 1) continue;
@@ -288,7 +288,9 @@ CCGQA_API ccgqa_status ccgqa_window_attention(const ccgqa_config* cfg, const ccg
   a.stats = stats;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!stream_allowed(st)) return CCGQA_ERR_INVALID_ARG;
-  const cudaError_t e = g.dtype == CCGQA_BF16 ? launch_window_simt<bf16>(a, st) : launch_window_simt<float>(a, st);
+  const cudaError_t e = g.dtype == CCGQA_F32         ? launch_window_simt<float>(a, st)
+                        : g.d >= 32 && g.G <= 128 ? launch_window_tc(a, st)
+                                                  : launch_window_simt<bf16>(a, st);
   return e == cudaSuccess ? CCGQA_OK : cuda_fail(e);
 }
 

@@ -1,0 +1,367 @@
+// Causal grouped-query attention of whole sequences over a sliding window with
+// sink tokens on the 5th-generation tensor core (bf16, d in {32, 64, 128},
+// groups of up to 128 heads).  ("Compressed Convolutional Attention", CCGQA: kv
+// heads shared by a group; the window and the sinks bound the keys a query
+// reads: s <= t and (s > t - window or s < sinks).)
+//
+// Query rows are packed per kv group as in the causal kernel: row r of a tile is
+// position t0 + r / G, head g G + r % G, gathered by a 5-D TMA box from any
+// strides; a tile holds floor(128 / G) positions, rows past them are zeroed
+// once.  One CTA owns T consecutive query tiles of one kv group and walks the
+// key pieces (64 keys) they see: the sinks' pieces, then the window's, whose first
+// key is the first one any of its rows sees: a TMA box may start at any row, so
+// a window of W keys costs W + (positions of the CTA) keys rounded up to 64, not
+// whole aligned tiles at both ends.
+//   warp 0      TMA producer: the query tiles once, then K/V pieces
+//   warps 1..T  one thread each issues the tcgen05.mma of one query tile:
+//                 S = Q K_k^T (SS, 128 x 64, TMEM), O += P V_k (TS, P in TMEM)
+//               S of piece k + 2 goes into the buffer P(k) was read from, so the
+//               softmax of piece k + 1 never waits for the products
+//   warps 4..   softmax, one thread per row: 2^(c s - m) with a running max m
+//               that is raised only when a row's partial sum overshoots, bf16 P
+//               into TMEM, the rare rescale of O, the division and the store
+// Masks are needed only at a window's first pieces, the diagonal and the sinks'
+// pieces: there a 64-bit set of visible columns is formed per row.
+// A row whose first pieces hold none of its keys starts from a running max of
+// -1e30; its first visible score overshoots, and the sums so far, of zeros, are
+// scaled by zero.
+//
+// No cluster multicast; every wait is bounded.
+#include "attn_math.cuh"
+#include "sm100.cuh"
+#include "window_tc.cuh"
+
+namespace ccgqa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kPiece = 64;
+// Every probability stays below this (times 64 keys): see exp_pass.
+constexpr float kSumLimit = 1024.0f;
+
+template <int D>
+struct FwdCfg : RowTiles<D> {
+  using R = RowTiles<D>;
+  static constexpr uint32_t kTileBytes = 128 * D * 2;         // one Q tile
+  static constexpr uint32_t kPieceBytes = kPiece * D * 2;     // one K or V piece
+  static constexpr uint32_t kPanelQ = 128 * R::kRowBytes;
+  static constexpr uint32_t kPanelK = kPiece * R::kRowBytes;
+  static constexpr int kStages = D == 128 ? 4 : (D == 64 ? 6 : 8);
+  static constexpr int kTiles = D == 32 ? 3 : 2;              // S buffers and sums fill TMEM
+  // one pair in kSoftEvery takes the FMA pipe's exponential (the best shares of
+  // the causal kernel, whose softmax this is)
+  static constexpr int kSoftEvery = D == 64 ? 3 : (D == 32 ? 5 : 4);
+  static constexpr int kThreads = 128 + 128 * kTiles;
+  static constexpr uint32_t kOffQ = 0;
+  static constexpr uint32_t kOffK = kTiles * kTileBytes;
+  static constexpr uint32_t kOffV = kOffK + kStages * kPieceBytes;
+  static constexpr uint32_t kOffBar = kOffV + kStages * kPieceBytes;
+  static constexpr size_t kSmem = kOffBar + 512 + 1024;
+  static constexpr uint32_t kTmemCols = 512;
+  static_assert(kTiles * 128 + kTiles * D <= 512, "TMEM columns");
+  __device__ static constexpr uint32_t col_s(int x, int h) { return x * 128 + h * 64; }
+  __device__ static constexpr uint32_t col_p(int x, int h) { return x * 128 + h * 64 + 32; }
+  __device__ static constexpr uint32_t col_o(int x) { return kTiles * 128 + x * D; }
+};
+
+template <int D>
+__global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1)
+    window_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WindowArgs a,
+                         int n_groups) {
+  pdl_enter();
+  using C = FwdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* kv_full = q_full + 1;                // [kStages]
+  uint64_t* kv_empty = kv_full + C::kStages;     // [kStages], one commit per tile
+  uint64_t* s_full = kv_empty + C::kStages;      // [tile][buffer] S ready
+  uint64_t* p_full = s_full + 2 * C::kTiles;     // [tile][buffer] P written (128 arrivals)
+  uint64_t* o_done = p_full + 2 * C::kTiles;     // [tile][buffer] its PV complete
+  uint64_t* drain = o_done + 2 * C::kTiles;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.G, BH = a.B * a.Hkv;
+  const int grp = n_groups - 1 - static_cast<int>(blockIdx.x) / BH;   // the longest first
+  const int bg = static_cast<int>(blockIdx.x) % BH;
+  const int b = bg / a.Hkv, g = bg % a.Hkv;
+  const int pos = 128 / G, rows_used = pos * G;
+  const int t0 = grp * C::kTiles * pos;
+  const int t_last = min(t0 + C::kTiles * pos, a.S) - 1;
+  const int lo = max(0, t0 - a.window + 1);      // first key of the window of any row
+  const int sinks = min(a.sinks, lo);            // sink keys before it
+  const int n_sink = (sinks + kPiece - 1) / kPiece;
+  const int n = n_sink + (t_last - lo) / kPiece + 1;
+  auto piece = [&](int k) { return k < n_sink ? k * kPiece : lo + (k - n_sink) * kPiece; };
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], C::kTiles);
+    }
+    for (int i = 0; i < 2 * C::kTiles; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(drain, C::kTiles);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  zero_unused_rows<D>(smem + C::kOffQ, C::kTiles, 128, rows_used);
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tensormap(&tmQ);
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+      mbar_arrive_expect_tx(q_full, C::kTiles * rows_used * D * 2);
+#pragma unroll
+      for (int x = 0; x < C::kTiles; ++x)
+#pragma unroll
+        for (int p = 0; p < C::kPanels; ++p)
+          tma_load_5d(smem + C::kOffQ + x * C::kTileBytes + p * C::kPanelQ, &tmQ, q_full, p * C::kPanelCols, 0, g,
+                      t0 + x * pos, b);
+      for (int k = 0; k < n; ++k) {
+        const int st = k % C::kStages;
+        if (!mbar_wait(&kv_empty[st], ((k / C::kStages) & 1) ^ 1, &abort_flag, a.dev_err)) break;
+        mbar_arrive_expect_tx(&kv_full[st], 2 * C::kPieceBytes);
+#pragma unroll
+        for (int p = 0; p < C::kPanels; ++p) {
+          tma_load_4d(smem + C::kOffK + st * C::kPieceBytes + p * C::kPanelK, &tmK, &kv_full[st], p * C::kPanelCols,
+                      piece(k), g, b);
+          tma_load_4d(smem + C::kOffV + st * C::kPieceBytes + p * C::kPanelK, &tmV, &kv_full[st], p * C::kPanelCols,
+                      piece(k), g, b);
+        }
+      }
+    }
+  } else if (warp >= 1 && warp <= C::kTiles) {
+    // ------------------------------------------------------------ MMA issuers
+    if (lane == 0) {
+      const int x = warp - 1;
+      const uint32_t idesc_s = make_idesc_bf16(128, kPiece, false);
+      const uint32_t idesc_o = make_idesc_bf16(128, D, true);
+      const uint32_t q_base = smem_addr(smem + C::kOffQ) + x * C::kTileBytes;
+      auto issue_s = [&](int k) {
+        mma_rows_by_rows<D>(tmem + C::col_s(x, k & 1), q_base, C::kPanelQ,
+                            smem_addr(smem + C::kOffK + k % C::kStages * C::kPieceBytes), C::kPanelK, idesc_s);
+        mma_commit(&s_full[x * 2 + (k & 1)]);
+      };
+      bool ok = mbar_wait(q_full, 0, &abort_flag, a.dev_err);
+      for (int k = 0; ok && k < 2 && k < n; ++k) {
+        ok = mbar_wait(&kv_full[k], 0, &abort_flag, a.dev_err);
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(k);
+      }
+      for (int k = 0; ok && k < n; ++k) {
+        const int sb = x * 2 + (k & 1);
+        if (!mbar_wait(&p_full[sb], (k >> 1) & 1, &abort_flag, a.dev_err)) break;
+        tc_fence_after();
+        mma_tmem_by_rows<D, kPiece>(tmem + C::col_o(x), tmem + C::col_p(x, k & 1),
+                                    smem_addr(smem + C::kOffV + k % C::kStages * C::kPieceBytes), C::kPanelK, idesc_o,
+                                    k == 0);
+        mma_commit(&o_done[sb]);
+        mma_commit(&kv_empty[k % C::kStages]);
+        if (k + 2 < n) {
+          if (!mbar_wait(&kv_full[(k + 2) % C::kStages], ((k + 2) / C::kStages) & 1, &abort_flag, a.dev_err) ||
+              !mbar_wait(&o_done[sb], (k >> 1) & 1, &abort_flag, a.dev_err))
+            break;
+          tc_fence_after();
+          issue_s(k + 2);
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int x = (warp - 4) >> 2;
+    const int q4 = warp & 3;
+    const int r = q4 * 32 + lane;                 // tile row == TMEM lane
+    const int t = t0 + x * pos + r / G, hl = r % G;
+    const bool row_ok = r < rows_used && t < a.S;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+    const float scale = kLog2e * rsqrtf(static_cast<float>(D));
+    const float2 scale2 = make_float2(scale, scale);
+    float m_used = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int k = 0; ok && k < n; ++k) {
+      const int sb = x * 2 + (k & 1);
+      // columns below end that are at least begin, or below first, are visible
+      const int kb = piece(k);
+      int begin = t - a.window + 1 - kb, end = min(t, a.S - 1) + 1 - kb, first = a.sinks - kb;
+      if (k < n_sink) {
+        begin = kPiece;
+        first = sinks - kb;
+      }
+      const bool whole = __all_sync(0xffffffffu, end >= kPiece && (begin <= 0 || first >= kPiece));
+      uint64_t seen = ~uint64_t(0);
+      if (!whole) seen = (below(first) | ~below(begin)) & below(end);
+      if (!mbar_wait(&s_full[sb], (k >> 1) & 1, &abort_flag, a.dev_err)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      auto load_s = [&](float (&sv)[64]) {
+        tmem_ld32(trow + C::col_s(x, k & 1), *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+        tmem_ld32(trow + C::col_s(x, k & 1) + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+        tmem_wait_ld();
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) sv[c] = (seen >> c) & 1 ? sv[c] : -INFINITY;
+        }
+      };
+      auto row_max = [&](const float (&sv)[64]) {
+        float mx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx[i] = sv[i];
+#pragma unroll
+        for (int c = 8; c < 64; ++c) mx[c & 7] = fmaxf(mx[c & 7], sv[c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], mx[i + 4]);
+        return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+      };
+      uint32_t pk[32];
+      // p = 2^(s scale - m_used) as bf16 pairs; returns the row's sum of p, or
+      // +inf when an argument of the software exponential passed its range
+      auto exp_pass = [&](const float (&sv)[64]) {
+        const float2 negm2 = make_float2(-m_used, -m_used);
+        const float2* s2 = reinterpret_cast<const float2*>(sv);
+        float2 lsum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float soft_max = -INFINITY;
+#pragma unroll
+        for (int c2 = 0; c2 < 32; ++c2) {
+          const float2 arg = ffma2(s2[c2], scale2, negm2);
+          float2 p;
+          if ((c2 % C::kSoftEvery) == 0) {
+            soft_max = fmax3(soft_max, arg.x, arg.y);
+            p = soft_exp2x2(arg);
+          } else {
+            p.x = fast_exp2(arg.x);
+            p.y = fast_exp2(arg.y);
+          }
+          lsum[c2 & 3] = fadd2(lsum[c2 & 3], p);
+          pk[c2] = pack_bf16x2(p.x, p.y);
+        }
+        const float2 a2 = fadd2(fadd2(lsum[0], lsum[1]), fadd2(lsum[2], lsum[3]));
+        return soft_max < kSoftArgMax ? a2.x + a2.y : INFINITY;
+      };
+      // The first piece sets the running max.  Later ones exponentiate against it
+      // as it stands; a row whose partial sum passes kSumLimit reloads S, which is
+      // still in TMEM, raises the running max and redoes the piece.
+      float part;
+      {
+        float sv[64];
+        load_s(sv);
+        if (k == 0) m_used = fmaxf(row_max(sv), -1e30f);
+        part = exp_pass(sv);
+      }
+      const bool redo = !(part <= kSumLimit);
+      bool need = false;
+      float factor = 1.f;
+      if (__any_sync(0xffffffffu, redo)) {
+        float sv[64];
+        load_s(sv);   // warp-wide
+        if (redo) {
+          const float m_new = row_max(sv);
+          factor = fast_exp2(m_used - m_new);
+          l *= factor;
+          m_used = m_new;
+          need = true;
+          part = exp_pass(sv);
+        }
+      }
+      l += part;
+      if (__any_sync(0xffffffffu, need) && k > 0) {
+        // O must hold every earlier piece: wait for the last PV of this tile
+        if (!mbar_wait(&o_done[x * 2 + ((k - 1) & 1)], ((k - 1) >> 1) & 1, &abort_flag, a.dev_err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(trow + C::col_o(x) + c * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+          tmem_st32(trow + C::col_o(x) + c * 32, o);
+        }
+      }
+      tmem_st32(trow + C::col_p(x, k & 1), pk);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[sb]);
+    }
+    // the last PV of this tile completes after all others
+    if (ok && mbar_wait(&o_done[x * 2 + ((n - 1) & 1)], ((n - 1) >> 1) & 1, &abort_flag, a.dev_err)) {
+      tc_fence_after();
+      const float inv_l = 1.f / l;
+      if (a.stats != nullptr && row_ok) a.stats[a.stat_row(bg, t, hl)] = -(m_used + log2f(l));
+      bf16* dst = static_cast<bf16*>(a.out.ptr) + b * a.out.batch + t * a.out.token + (g * G + hl) * a.out.head;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(trow + C::col_o(x) + c * 32, o);
+        tmem_wait_ld();
+        if (row_ok) store32(dst + c * 32, o, inv_l);
+      }
+    }
+  }
+
+  if (abort_flag && warp >= 1 && warp <= C::kTiles && lane == 0) drain_mmas(drain);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch_fwd(const WindowArgs& a, cudaStream_t stream) {
+  using C = FwdCfg<D>;
+  CUtensorMap tmQ, tmK, tmV;
+  if (!packed_rows_map(&tmQ, a.q, a, 128 / a.G) || !key_rows_map(&tmK, a.k, a, kPiece) ||
+      !key_rows_map(&tmV, a.v, a, kPiece))
+    return cudaErrorInvalidValue;
+  const int per_cta = C::kTiles * (128 / a.G);
+  const int64_t n_groups = (a.S + per_cta - 1) / per_cta;
+  const int64_t grid = n_groups * a.B * a.Hkv;
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_fwd_tc_kernel<D>), static_cast<int>(C::kSmem));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(window_fwd_tc_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), C::kSmem, stream, tmQ,
+                 tmK, tmV, a, static_cast<int>(n_groups));
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_tc(const WindowArgs& a, cudaStream_t stream) {
+  if (a.G > 128) return cudaErrorInvalidValue;
+  switch (a.d) {
+    case 32: return launch_fwd<32>(a, stream);
+    case 64: return launch_fwd<64>(a, stream);
+    case 128: return launch_fwd<128>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace ccgqa

@@ -309,6 +309,8 @@ struct WindowArgs {
     return bg * ld + (pos ? static_cast<int64_t>(t / pos) * 64 + t % pos * G : static_cast<int64_t>(t) * G) + hl;
   }
 };
+// bf16, d in {32, 64, 128}, G <= 128: tcgen05.
+cudaError_t launch_window_tc(const WindowArgs& a, cudaStream_t stream);
 template <typename T>
 cudaError_t launch_window_simt(const WindowArgs& a, cudaStream_t stream);
 template <typename T>

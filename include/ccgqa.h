@@ -442,7 +442,8 @@ CCGQA_API size_t ccgqa_window_attention_stats_size(const ccgqa_config* cfg, int3
  *  - stats: nullable, ccgqa_window_attention_stats_size floats, 256-byte
  *    aligned; needed by the backward pass.
  *  - Only key tiles that a query tile sees are visited: work and time grow
- *    with seq_len * (window + sinks).  CUDA cores, fp32 throughout.
+ *    with seq_len * (window + sinks).  bf16 with d >= 32 and G <= 128: tcgen05,
+ *    probabilities rounded to bf16, fp32 sums; otherwise CUDA cores, fp32.
  *  - k and v must be finite: a key that is masked for a query has weight zero,
  *    but zero times an infinity or NaN in its tile is NaN. */
 CCGQA_API ccgqa_status ccgqa_window_attention(const ccgqa_config* cfg, const ccgqa_window* win,
