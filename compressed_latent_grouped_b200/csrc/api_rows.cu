@@ -129,8 +129,13 @@ bool window_args(const Geo& g, const ccgqa_window* win, int B, int S, const ccgq
   return true;
 }
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255) == 0; }
+bool window_tc(const Geo& g, int max_group) { return g.dtype == CCGQA_BF16 && g.d >= 32 && g.G <= max_group; }
+// dsum, then the tensor-core path's partial sums.
+size_t window_dsum_bytes(const Geo& g, int64_t B, int64_t S) {
+  return up256(static_cast<size_t>(B * g.Hkv * stat_rows(g, S)) * sizeof(float));
+}
 size_t window_bwd_workspace(const Geo& g, int64_t B, int64_t S) {
-  return static_cast<size_t>(B * g.Hkv * stat_rows(g, S)) * sizeof(float);
+  return window_dsum_bytes(g, B, S) + (window_tc(g, 64) ? window_bwd_tc_part_floats(g.d) * sizeof(float) : 0);
 }
 
 bool window_ok(const ccgqa_window* w) { return !w || (w->window >= 0 && w->sinks >= 0); }
@@ -288,9 +293,9 @@ CCGQA_API ccgqa_status ccgqa_window_attention(const ccgqa_config* cfg, const ccg
   a.stats = stats;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!stream_allowed(st)) return CCGQA_ERR_INVALID_ARG;
-  const cudaError_t e = g.dtype == CCGQA_F32         ? launch_window_simt<float>(a, st)
-                        : g.d >= 32 && g.G <= 128 ? launch_window_tc(a, st)
-                                                  : launch_window_simt<bf16>(a, st);
+  const cudaError_t e = window_tc(g, 128)          ? launch_window_tc(a, st)
+                        : g.dtype == CCGQA_BF16 ? launch_window_simt<bf16>(a, st)
+                                                : launch_window_simt<float>(a, st);
   return e == cudaSuccess ? CCGQA_OK : cuda_fail(e);
 }
 
@@ -329,7 +334,9 @@ CCGQA_API ccgqa_status ccgqa_window_attention_backward(
   a.dq = rows_of(*dq, batch, seq_len, g.Hq);
   a.dk = rows_of(*dk, batch, seq_len, g.Hkv);
   a.dv = rows_of(*dv, batch, seq_len, g.Hkv);
-  const cudaError_t e =
-      g.dtype == CCGQA_BF16 ? launch_window_bwd_simt<bf16>(a, st) : launch_window_bwd_simt<float>(a, st);
+  a.part = a.dsum + window_dsum_bytes(g, batch, seq_len) / sizeof(float);
+  const cudaError_t e = window_tc(g, 64)           ? launch_window_bwd_tc(a, st)
+                        : g.dtype == CCGQA_BF16 ? launch_window_bwd_simt<bf16>(a, st)
+                                                : launch_window_bwd_simt<float>(a, st);
   return e == cudaSuccess ? CCGQA_OK : cuda_fail(e);
 }

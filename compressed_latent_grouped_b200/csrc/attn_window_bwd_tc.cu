@@ -1,0 +1,812 @@
+// Gradients of the window attention on the 5th-generation tensor core (bf16, d
+// in {32, 64, 128}, groups of up to 64 heads).  With c = log2(e) / sqrt(d):
+//   P = 2^(c S - lse), S = q k^T;  dP = dO v^T;  dS = P (dP - D), D = rowsum(dO o)
+//   dq = dS k / sqrt(d);  dk = dS^T q / sqrt(d);  dv = P^T dO   (group sums)
+// Sums are fp32; P and dS are rounded to bf16 for the products; each gradient is
+// rounded once, at its store.
+//
+// Two kernels, each with one 128-row tile per CTA and blocks of 128 columns, so
+// that a product reads as many bytes of its A as of its B from shared memory (at
+// 128 x 64 or 128 x 32 the A operand, read again for every block, bounds it):
+//   dq pass   rows = packed queries (two groups of 64 rows, each 64 / G
+//             positions with their G heads), columns = keys
+//   dkv pass  rows = keys, columns = packed queries: a block holds rows of all
+//             heads of the group, so the group's sum comes from the product
+// Warp 0 loads (TMA), one thread of warp 1 issues the products, sixteen warps do
+// the scores: four per TMEM quadrant, each 32 columns of its 32 rows, so that four
+// warps per scheduler hide one another's latencies (with one warp per scheduler
+// and row these kernels ran at a third of the issue rate).
+// TMEM columns: slots of 128 hold S, dP and, in each warp's own columns, the bf16
+// P and dS over them.  With three slots the scores of block k + 1 are computed
+// while block k is worked: S(k) in slot 2k mod 3, dP(k) in slot 2k + 1 mod 3.  The
+// dkv pass at d = 128 has two (dK and dV take the other half), and the scores of
+// the next block follow the products that free their slot.
+//
+// The dkv pass's work is cut evenly: the blocks of all key tiles, in order, are
+// shared out to one CTA per SM; a tile whose blocks end up in several CTAs leaves
+// fp32 partial sums that a third kernel adds in the order of the CTAs, so equal
+// calls give equal bits, windows and sinks of any shape fill the GPU, and only
+// the tiles at the cuts cost extra traffic.
+//
+// No cluster multicast; every wait is bounded.
+#include <algorithm>
+
+#include "window_tc.cuh"
+
+namespace ccgqa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kRows = 128;                 // rows of a tile, columns of a block
+constexpr int kSoftWarps = 16;
+constexpr int kBwdThreads = 128 + 32 * kSoftWarps;
+constexpr int kMaxCtas = 160;              // of the dkv pass
+
+template <int D>
+struct BwdCfg : RowTiles<D> {
+  using R = RowTiles<D>;
+  static constexpr uint32_t kTile = kRows * D * 2;
+  static constexpr uint32_t kPanel = kRows * R::kRowBytes;
+  // dq pass: Q and dO, rings of K and V
+  static constexpr int kKStages = D == 128 ? 3 : 4, kVStages = D == 128 ? 2 : 4;
+  static constexpr uint32_t kQOffQ = 0, kQOffDO = kTile, kQOffK = 2 * kTile;
+  static constexpr uint32_t kQOffV = kQOffK + kKStages * kTile;
+  static constexpr uint32_t kQOffBar = kQOffV + kVStages * kTile;
+  static constexpr size_t kQSmem = kQOffBar + 512 + 1024;
+  // dkv pass: K and V, rings of Q with its lse and dO with its D
+  static constexpr int kRing = D == 128 ? 2 : 4;
+  static constexpr uint32_t kKOffK = 0, kKOffV = kTile, kKOffQ = 2 * kTile;
+  static constexpr uint32_t kKOffDO = kKOffQ + kRing * kTile;
+  static constexpr uint32_t kKOffL = kKOffDO + kRing * kTile;
+  static constexpr uint32_t kKOffD = kKOffL + kRing * kRows * 4;
+  static constexpr uint32_t kKOffBar = kKOffD + kRing * kRows * 4;
+  static constexpr size_t kKSmem = kKOffBar + 512 + 1024;
+  static constexpr int kSlots = D == 128 ? 2 : 3;             // dkv pass
+  static constexpr uint32_t kColQ = 3 * kRows;                // dq pass: sums
+  static constexpr uint32_t kColV = kSlots * kRows, kColK = kColV + D;
+  static_assert(kColK + D <= 512 && kColQ + D <= 512, "TMEM columns");
+  static_assert(kQSmem + 1280 <= 227 * 1024 && kKSmem + 256 <= 227 * 1024, "shared memory, with the static part");
+};
+
+// acc (+)= A B: A 128 x 128 bf16 in TMEM, 32 columns of it at the head of every 32
+// TMEM columns; B 128 rows at b_base read MN-major.
+template <int D>
+__device__ __forceinline__ void mma_slot_by_rows(uint32_t acc, uint32_t slot, uint32_t b_base, uint32_t idesc, bool first) {
+  using C = BwdCfg<D>;
+#pragma unroll
+  for (int k = 0; k < kRows / 16; ++k)
+    mma_ts(acc, slot + (k >> 1) * 32 + (k & 1) * 8,
+           make_smem_desc(b_base + k * 16 * C::kRowBytes, C::kPanel, C::kSbo, C::kSwz), idesc, !first || k > 0 ? 1u : 0u);
+}
+
+// Arrival of a warp whose TMEM accesses have completed.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// 2^x on 32 values; one pair in four on the FMA pipe.
+__device__ __forceinline__ void exp2_32(float (&p)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    if (e % 8 == 0) {
+      const float2 y = soft_exp2x2(make_float2(p[e], p[e + 1]));
+      p[e] = y.x;
+      p[e + 1] = y.y;
+    } else {
+      p[e] = fast_exp2(p[e]);
+      p[e + 1] = fast_exp2(p[e + 1]);
+    }
+  }
+}
+
+// ================================================================ dq pass
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
+                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ WindowArgs a, int n_tiles) {
+  pdl_enter();
+  using C = BwdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kQOffBar);
+  uint64_t* k_full = q_full + 1;
+  uint64_t* k_empty = k_full + C::kKStages;
+  uint64_t* v_full = k_empty + C::kKStages;
+  uint64_t* v_empty = v_full + C::kVStages;
+  uint64_t* s_full = v_empty + C::kVStages;      // [2], by block
+  uint64_t* s_read = s_full + 2;                 // [2], one arrival per warp
+  uint64_t* dp_full = s_read + 2;                // [2]
+  uint64_t* ds_full = dp_full + 2;               // [2], one arrival per warp
+  uint64_t* dq_done = ds_full + 2;
+  uint64_t* fin = dq_done + 1;
+  uint64_t* drain = fin + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  __shared__ int abort_flag;
+  __shared__ float dpart[2][kRows];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.G, BH = a.B * a.Hkv;
+  const int tile = n_tiles - 1 - static_cast<int>(blockIdx.x) / BH;
+  const int bg = static_cast<int>(blockIdx.x) % BH;
+  const int b = bg / a.Hkv, g = bg % a.Hkv;
+  const int pos = 64 / G, used = pos * G;         // positions and rows of a group of 64 rows
+  const int t0 = tile * 2 * pos;
+  const int t_last = min(t0 + 2 * pos, a.S) - 1;
+  const int lo = max(0, t0 - a.window + 1);
+  const int sinks = min(a.sinks, lo);
+  const int n_sink = (sinks + kRows - 1) / kRows;
+  const int n = n_sink + (t_last - lo) / kRows + 1;
+  auto block = [&](int k) { return k < n_sink ? k * kRows : lo + (k - n_sink) * kRows; };
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < C::kKStages; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < C::kVStages; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_read[i], kSoftWarps);
+      mbar_init(&dp_full[i], 1);
+      mbar_init(&ds_full[i], kSoftWarps);
+    }
+    mbar_init(dq_done, 1);
+    mbar_init(fin, 1);
+    mbar_init(drain, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  // Q and dO: two tiles, panels of two 64-row groups each
+  zero_unused_rows<D>(smem + C::kQOffQ, 4, 64, used);
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto slot_s = [&](int k) { return tmem + static_cast<uint32_t>(2 * k % 3) * kRows; };
+  auto slot_dp = [&](int k) { return tmem + static_cast<uint32_t>((2 * k + 1) % 3) * kRows; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tensormap(&tmQ);
+      prefetch_tensormap(&tmDO);
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+      mbar_arrive_expect_tx(q_full, 4 * used * D * 2);
+#pragma unroll
+      for (int p = 0; p < C::kPanels; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t off = p * C::kPanel + j * 64 * C::kRowBytes;
+          tma_load_5d(smem + C::kQOffQ + off, &tmQ, q_full, p * C::kPanelCols, 0, g, t0 + j * pos, b);
+          tma_load_5d(smem + C::kQOffDO + off, &tmDO, q_full, p * C::kPanelCols, 0, g, t0 + j * pos, b);
+        }
+      for (int k = 0; k < n; ++k) {
+        const int ks = k % C::kKStages, vs = k % C::kVStages;
+        if (!mbar_wait(&k_empty[ks], ((k / C::kKStages) & 1) ^ 1, &abort_flag, a.dev_err)) break;
+        mbar_arrive_expect_tx(&k_full[ks], C::kTile);
+#pragma unroll
+        for (int p = 0; p < C::kPanels; ++p)
+          tma_load_4d(smem + C::kQOffK + ks * C::kTile + p * C::kPanel, &tmK, &k_full[ks], p * C::kPanelCols, block(k), g, b);
+        if (!mbar_wait(&v_empty[vs], ((k / C::kVStages) & 1) ^ 1, &abort_flag, a.dev_err)) break;
+        mbar_arrive_expect_tx(&v_full[vs], C::kTile);
+#pragma unroll
+        for (int p = 0; p < C::kPanels; ++p)
+          tma_load_4d(smem + C::kQOffV + vs * C::kTile + p * C::kPanel, &tmV, &v_full[vs], p * C::kPanelCols, block(k), g, b);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc_s = make_idesc_bf16(128, kRows, false), idesc_o = make_idesc_bf16(128, D, true);
+      const uint32_t q_base = smem_addr(smem + C::kQOffQ), do_base = smem_addr(smem + C::kQOffDO);
+      auto k_base = [&](int k) { return smem_addr(smem + C::kQOffK + k % C::kKStages * C::kTile); };
+      auto issue_s = [&](int k) {
+        if (!mbar_wait(&k_full[k % C::kKStages], (k / C::kKStages) & 1, &abort_flag, a.dev_err)) return false;
+        tc_fence_after();
+        mma_rows_by_rows<D>(slot_s(k), q_base, C::kPanel, k_base(k), C::kPanel, idesc_s);
+        mma_commit(&s_full[k & 1]);
+        return true;
+      };
+      auto issue_dp = [&](int k) {
+        if (!mbar_wait(&v_full[k % C::kVStages], (k / C::kVStages) & 1, &abort_flag, a.dev_err)) return false;
+        tc_fence_after();
+        mma_rows_by_rows<D>(slot_dp(k), do_base, C::kPanel, smem_addr(smem + C::kQOffV + k % C::kVStages * C::kTile),
+                            C::kPanel, idesc_s);
+        mma_commit(&dp_full[k & 1]);
+        mma_commit(&v_empty[k % C::kVStages]);
+        return true;
+      };
+      bool ok = mbar_wait(q_full, 0, &abort_flag, a.dev_err) && issue_s(0) && issue_dp(0) && (n < 2 || issue_s(1));
+      for (int k = 0; ok && k < n; ++k) {
+        // dP(k + 1) takes the slot of S(k) once it has been read, S(k + 2) that
+        // of dS(k) once dQ has read it
+        if (k + 1 < n && !(mbar_wait(&s_read[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err) && issue_dp(k + 1))) break;
+        if (!mbar_wait(&ds_full[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err)) break;
+        tc_fence_after();
+        mma_slot_by_rows<D>(tmem + C::kColQ, slot_dp(k), k_base(k), idesc_o, k == 0);
+        mma_commit(dq_done);
+        mma_commit(&k_empty[k % C::kKStages]);
+        if (k + 1 == n) mma_commit(fin);
+        if (k + 2 < n && !(mbar_wait(dq_done, k & 1, &abort_flag, a.dev_err) && issue_s(k + 2))) break;
+        if (k + 2 >= n && k + 1 < n && !mbar_wait(dq_done, k & 1, &abort_flag, a.dev_err)) break;
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ scores
+    const int w = (warp - 4) >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane;                 // tile row == TMEM lane
+    const int u = r & 63, t = t0 + (r >> 6) * pos + u / G, hl = u % G;
+    const bool row_ok = u < used && t < a.S;
+    const uint32_t trow = (static_cast<uint32_t>(q4 * 32) << 16) + w * 32;
+    const int64_t srow = bg * a.ld + static_cast<int64_t>(tile) * kRows + r;
+    float nlse = 0.f, nd = 0.f;   // -lse, -D
+    {
+      // D = rowsum(dO o): two of a row's four warps form one half of it, two the other
+      float acc = 0.f;
+      if (row_ok) {
+        nlse = a.stats[srow];
+        const int h = g * G + hl;
+        const bf16* x = static_cast<const bf16*>(a.dout.ptr) + b * a.dout.batch + t * a.dout.token + h * a.dout.head + (w & 1) * (D / 2);
+        const bf16* y = static_cast<const bf16*>(a.out.ptr) + b * a.out.batch + t * a.out.token + h * a.out.head + (w & 1) * (D / 2);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint4 x4 = *reinterpret_cast<const uint4*>(x + i * 8), y4 = *reinterpret_cast<const uint4*>(y + i * 8);
+          const __nv_bfloat162* x2 = reinterpret_cast<const __nv_bfloat162*>(&x4);
+          const __nv_bfloat162* y2 = reinterpret_cast<const __nv_bfloat162*>(&y4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 xf = __bfloat1622float2(x2[e]), yf = __bfloat1622float2(y2[e]);
+            acc = fmaf(xf.x, yf.x, acc);
+            acc = fmaf(xf.y, yf.y, acc);
+          }
+        }
+      }
+      if (w < 2) dpart[w][r] = acc;
+      named_barrier_sync(1, 32 * kSoftWarps);
+      nd = -(dpart[0][r] + dpart[1][r]);
+      if (row_ok && w == 0) a.dsum[srow] = nd;
+    }
+    const float c = kLog2e * rsqrtf(static_cast<float>(D));
+    const float2 c2 = make_float2(c, c), nl2 = make_float2(nlse, nlse), nd2 = make_float2(nd, nd);
+    bool ok = true;
+    for (int k = 0; k < n; ++k) {
+      const int kb = block(k) + w * 32;
+      int begin = t - a.window + 1 - kb, end = min(t, a.S - 1) + 1 - kb, first = a.sinks - kb;
+      if (k < n_sink) {
+        begin = 32;
+        first = sinks - kb;
+      }
+      if (!row_ok) end = 0;
+      const uint32_t seen = (below32(first) | ~below32(begin)) & below32(end);
+      const bool whole = __all_sync(0xffffffffu, seen == ~0u), none = __all_sync(0xffffffffu, seen == 0u);
+      if (!mbar_wait(&s_full[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float p[32];
+      if (!none) {
+        tmem_ld32(slot_s(k) + trow, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
+        tmem_wait_ld();
+      }
+      warp_arrive(&s_read[k & 1], lane);
+      if (!none) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 y = ffma2(make_float2(p[e], p[e + 1]), c2, nl2);
+          p[e] = y.x;
+          p[e + 1] = y.y;
+        }
+        exp2_32(p);
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) p[e] = (seen >> e) & 1 ? p[e] : 0.f;
+        }
+      }
+      if (!mbar_wait(&dp_full[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t ds[16];
+      if (none) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ds[e] = 0;
+      } else {
+        uint32_t dp[32];
+        tmem_ld32(slot_dp(k) + trow, dp);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 y = fmul2(make_float2(p[2 * e], p[2 * e + 1]),
+                                 fadd2(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), nd2));
+          ds[e] = pack_bf16x2(y.x, y.y);
+        }
+      }
+      tmem_st16(slot_dp(k) + trow, ds);
+      tmem_wait_st();
+      warp_arrive(&ds_full[k & 1], lane);
+    }
+    if (ok && mbar_wait(fin, 0, &abort_flag, a.dev_err)) {
+      tc_fence_after();
+      const float sc = rsqrtf(static_cast<float>(D));
+      bf16* dst = static_cast<bf16*>(a.dq.ptr) + b * a.dq.batch + t * a.dq.token + (g * G + hl) * a.dq.head;
+      // each warp 32 columns: at d < 128 the first D / 32 of a row's four
+      if (w < D / 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem + C::kColQ + trow, v);
+        tmem_wait_ld();
+        if (row_ok) store32(dst + w * 32, v, sc);
+      }
+    }
+  }
+
+  if (abort_flag && warp == 1 && lane == 0) drain_mmas(drain);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ================================================================ dkv pass
+// Key tiles see the query groups (64 rows, pos positions) [first, last].
+struct DkvPlan {
+  int pos, n_tiles, n_ctas, n_split;
+  // CTA i works the blocks from start[i] up to start[i + 1]: x = (sequence, kv
+  // head) n_tiles + tile, y = block of the tile
+  int2 start[kMaxCtas + 1];
+  // tiles with several CTAs: tile, first and last CTA
+  int3 split[kMaxCtas];
+};
+__host__ __device__ inline int2 dkv_groups(int tile, int S, int window, int sinks, int pos) {
+  const int k0 = tile * kRows;
+  const long long reach = static_cast<long long>(k0) + kRows - 1 + window - 1;
+  const int t_max = k0 < sinks || reach > S - 1 ? S - 1 : static_cast<int>(reach);
+  return make_int2(k0 / pos, t_max / pos);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    window_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
+                         const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                         const __grid_constant__ WindowArgs a, const __grid_constant__ DkvPlan plan) {
+  pdl_enter();
+  using C = BwdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::kKOffBar);
+  uint64_t* kv_empty = kv_full + 1;
+  uint64_t* q_full = kv_empty + 1;               // [kRing] Q and lse
+  uint64_t* q_empty = q_full + C::kRing;         // [kRing] dK issued, and lse read by every warp
+  uint64_t* do_full = q_empty + C::kRing;        // [kRing] dO and D
+  uint64_t* do_empty = do_full + C::kRing;
+  uint64_t* s_full = do_empty + C::kRing;        // [2], by block
+  uint64_t* dp_full = s_full + 2;                // [2]
+  uint64_t* p_full = dp_full + 2;                // [2], one arrival per warp
+  uint64_t* ds_full = p_full + 2;                // [2], one arrival per warp
+  uint64_t* out_done = ds_full + 2;              // the issuer's own: dV or dK complete
+  uint64_t* fin = out_done + 1;                  // a segment's sums complete
+  uint64_t* acc_free = fin + 1;                  // its sums read, one arrival per warp
+  uint64_t* drain = acc_free + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.G, pos = plan.pos, used = pos * G;
+  const int2 from = plan.start[blockIdx.x], to = plan.start[blockIdx.x + 1];
+  // the CTA's segments: (tile, blocks [y0, y1) of n)
+  struct Seg {
+    int x, tile, b, g, g0, g1, n, y0, y1;
+  };
+  auto segment = [&](int x, Seg* s) {
+    if (x > to.x || (x == to.x && to.y == 0)) return false;
+    s->x = x;
+    s->tile = x % plan.n_tiles;
+    const int bg = x / plan.n_tiles;
+    s->b = bg / a.Hkv;
+    s->g = bg % a.Hkv;
+    const int2 gr = dkv_groups(s->tile, a.S, a.window, a.sinks, pos);
+    s->g0 = gr.x;
+    s->g1 = gr.y;
+    s->n = (gr.y - gr.x) / 2 + 1;
+    s->y0 = x == from.x ? from.y : 0;
+    s->y1 = x == to.x ? to.y : s->n;
+    return true;
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    mbar_init(kv_empty, 1);
+    for (int s = 0; s < C::kRing; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+      mbar_init(&do_full[s], 1);
+      mbar_init(&do_empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&dp_full[i], 1);
+      mbar_init(&p_full[i], kSoftWarps);
+      mbar_init(&ds_full[i], kSoftWarps);
+    }
+    mbar_init(out_done, 1);
+    mbar_init(fin, 1);
+    mbar_init(acc_free, kSoftWarps);
+    mbar_init(drain, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  zero_unused_rows<D>(smem + C::kKOffQ, 4 * C::kRing, 64, used);   // Q and dO rings, two groups each
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto slot_s = [&](int i) { return tmem + static_cast<uint32_t>(C::kSlots == 3 ? 2 * i % 3 : 0) * kRows; };
+  auto slot_dp = [&](int i) { return tmem + static_cast<uint32_t>(C::kSlots == 3 ? (2 * i + 1) % 3 : 1) * kRows; };
+
+  // i counts the CTA's blocks over all its segments
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tensormap(&tmQ);
+      prefetch_tensormap(&tmDO);
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+      int i = 0, n_seg = 0;
+      bool ok = true;
+      Seg s;
+      for (int x = from.x; ok && segment(x, &s); ++x, ++n_seg) {
+        if (!(ok = mbar_wait(kv_empty, (n_seg & 1) ^ 1, &abort_flag, a.dev_err))) break;
+        mbar_arrive_expect_tx(kv_full, 2 * C::kTile);
+#pragma unroll
+        for (int p = 0; p < C::kPanels; ++p) {
+          tma_load_4d(smem + C::kKOffK + p * C::kPanel, &tmK, kv_full, p * C::kPanelCols, s.tile * kRows, s.g, s.b);
+          tma_load_4d(smem + C::kKOffV + p * C::kPanel, &tmV, kv_full, p * C::kPanelCols, s.tile * kRows, s.g, s.b);
+        }
+        const int64_t srow = static_cast<int64_t>(s.b * a.Hkv + s.g) * a.ld;
+        for (int y = s.y0; ok && y < s.y1; ++y, ++i) {
+          const int st = i % C::kRing, par = ((i / C::kRing) & 1) ^ 1;
+          // both groups of rows are loaded (zeros past the sequence: a masked row's
+          // products have to be finite), the statistics of those that exist
+          const int grp = s.g0 + 2 * y, n_stat = min(2, (a.S + pos - 1) / pos - grp);
+          auto load = [&](uint32_t off, uint32_t stat_off, const CUtensorMap* tm, const float* stat, uint64_t* full) {
+            mbar_arrive_expect_tx(full, 2 * used * D * 2 + n_stat * 256);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+              for (int p = 0; p < C::kPanels; ++p)
+                tma_load_5d(smem + off + st * C::kTile + p * C::kPanel + j * 64 * C::kRowBytes, tm, full, p * C::kPanelCols, 0,
+                            s.g, (grp + j) * pos, s.b);
+              if (j < n_stat)
+                bulk_load(smem + stat_off + st * kRows * 4 + j * 256, stat + srow + static_cast<int64_t>(grp + j) * 64, 256, full);
+            }
+          };
+          if (!(ok = mbar_wait(&q_empty[st], par, &abort_flag, a.dev_err))) break;
+          load(C::kKOffQ, C::kKOffL, &tmQ, a.stats, &q_full[st]);
+          if (!(ok = mbar_wait(&do_empty[st], par, &abort_flag, a.dev_err))) break;
+          load(C::kKOffDO, C::kKOffD, &tmDO, a.dsum, &do_full[st]);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc_s = make_idesc_bf16(128, kRows, false), idesc_o = make_idesc_bf16(128, D, true);
+      const uint32_t k_base = smem_addr(smem + C::kKOffK), v_base = smem_addr(smem + C::kKOffV);
+      auto q_base = [&](int i) { return smem_addr(smem + C::kKOffQ + i % C::kRing * C::kTile); };
+      auto do_base = [&](int i) { return smem_addr(smem + C::kKOffDO + i % C::kRing * C::kTile); };
+      auto issue_s = [&](int i) {
+        if (!mbar_wait(&q_full[i % C::kRing], (i / C::kRing) & 1, &abort_flag, a.dev_err)) return false;
+        tc_fence_after();
+        mma_rows_by_rows<D>(slot_s(i), k_base, C::kPanel, q_base(i), C::kPanel, idesc_s);
+        mma_commit(&s_full[i & 1]);
+        return true;
+      };
+      auto issue_dp = [&](int i) {
+        if (!mbar_wait(&do_full[i % C::kRing], (i / C::kRing) & 1, &abort_flag, a.dev_err)) return false;
+        tc_fence_after();
+        mma_rows_by_rows<D>(slot_dp(i), v_base, C::kPanel, do_base(i), C::kPanel, idesc_s);
+        mma_commit(&dp_full[i & 1]);
+        return true;
+      };
+      int i = 0, n_seg = 0, outs = 0;   // outs: completions of out_done waited for
+      bool ok = true;
+      Seg s;
+      for (int x = from.x; ok && segment(x, &s); ++x, ++n_seg) {
+        const int i0 = i, i1 = i + s.y1 - s.y0;
+        ok = (n_seg == 0 || mbar_wait(acc_free, (n_seg - 1) & 1, &abort_flag, a.dev_err)) &&
+             mbar_wait(kv_full, n_seg & 1, &abort_flag, a.dev_err) && issue_s(i) && issue_dp(i) &&
+             (C::kSlots == 2 || i + 1 >= i1 || issue_s(i + 1));
+        for (; ok && i < i1; ++i) {
+          if (!(ok = mbar_wait(&p_full[i & 1], (i >> 1) & 1, &abort_flag, a.dev_err))) break;
+          tc_fence_after();
+          mma_slot_by_rows<D>(tmem + C::kColV, slot_s(i), do_base(i), idesc_o, i == i0);
+          mma_commit(out_done);
+          // P's slot, once dV has read it: dP(i + 1), or with two slots S(i + 1)
+          if (!(ok = mbar_wait(out_done, outs++ & 1, &abort_flag, a.dev_err))) break;
+          if (i + 1 < i1 && !(ok = C::kSlots == 3 ? issue_dp(i + 1) : issue_s(i + 1))) break;
+          if (!(ok = mbar_wait(&ds_full[i & 1], (i >> 1) & 1, &abort_flag, a.dev_err))) break;
+          tc_fence_after();
+          // dV and every score have read dO(i); D(i) has been read before ds_full
+          mma_commit(&do_empty[i % C::kRing]);
+          mma_slot_by_rows<D>(tmem + C::kColK, slot_dp(i), q_base(i), idesc_o, i == i0);
+          mma_commit(out_done);
+          mma_commit(&q_empty[i % C::kRing]);
+          if (i + 1 == i1) {
+            mma_commit(fin);
+            mma_commit(kv_empty);
+          }
+          if (!(ok = mbar_wait(out_done, outs++ & 1, &abort_flag, a.dev_err))) break;
+          if (C::kSlots == 3 ? i + 2 < i1 && !(ok = issue_s(i + 2)) : i + 1 < i1 && !(ok = issue_dp(i + 1))) break;
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ scores
+    const int w = (warp - 4) >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane;                 // key row == TMEM lane
+    const uint32_t trow = (static_cast<uint32_t>(q4 * 32) << 16) + w * 32;
+    const float c = kLog2e * rsqrtf(static_cast<float>(D));
+    const float2 c2 = make_float2(c, c);
+    int i = 0, n_seg = 0;
+    bool ok = true;
+    Seg s;
+    for (int x = from.x; ok && segment(x, &s); ++x, ++n_seg) {
+      const int key = s.tile * kRows + r;
+      // positions [key, stop) see the key
+      const int stop = key >= a.S ? 0 : (key < a.sinks ? a.S : static_cast<int>(min(static_cast<int64_t>(a.S), static_cast<int64_t>(key) + a.window)));
+      for (int y = s.y0; y < s.y1; ++y, ++i) {
+        const int grp = s.g0 + 2 * y + (w >> 1);
+        const int tg = min(grp, s.g1 + 1) * pos;   // a group past the last one: no position is left
+        // rows of the group, here from its row 32 (w & 1): visible in [begin, end)
+        const int begin = max(-1, min(key - tg, pos)) * G - (w & 1) * 32;
+        const int end = grp > s.g1 ? 0 : max(0, min(stop - tg, pos)) * G - (w & 1) * 32;
+        const uint32_t seen = below32(end) & ~below32(begin);
+        const bool whole = __all_sync(0xffffffffu, seen == ~0u), none = __all_sync(0xffffffffu, seen == 0u);
+        const int st = i % C::kRing;
+        if (!mbar_wait(&s_full[i & 1], (i >> 1) & 1, &abort_flag, a.dev_err) ||
+            !mbar_wait(&q_full[st], (i / C::kRing) & 1, &abort_flag, a.dev_err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float p[32];
+        uint32_t pk[16];
+        if (none) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = 0;
+        } else {
+          tmem_ld32(slot_s(i) + trow, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
+          const float4* nl = reinterpret_cast<const float4*>(smem + C::kKOffL + st * kRows * 4) + w * 8;
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 l4 = nl[e / 4];
+            const float2 y0 = ffma2(make_float2(p[e], p[e + 1]), c2, make_float2(l4.x, l4.y));
+            const float2 y1 = ffma2(make_float2(p[e + 2], p[e + 3]), c2, make_float2(l4.z, l4.w));
+            p[e] = y0.x;
+            p[e + 1] = y0.y;
+            p[e + 2] = y1.x;
+            p[e + 3] = y1.y;
+          }
+          exp2_32(p);
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) p[e] = (seen >> e) & 1 ? p[e] : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(p[2 * e], p[2 * e + 1]);
+        }
+        tmem_st16(slot_s(i) + trow, pk);
+        tmem_wait_st();
+        warp_arrive(&p_full[i & 1], lane);
+        if (!mbar_wait(&dp_full[i & 1], (i >> 1) & 1, &abort_flag, a.dev_err) ||
+            !mbar_wait(&do_full[st], (i / C::kRing) & 1, &abort_flag, a.dev_err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (!none) {
+          uint32_t dp[32];
+          tmem_ld32(slot_dp(i) + trow, dp);
+          const float4* nd = reinterpret_cast<const float4*>(smem + C::kKOffD + st * kRows * 4) + w * 8;
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 d4 = nd[e / 4];
+            const float2 y0 = fmul2(make_float2(p[e], p[e + 1]),
+                                    fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), make_float2(d4.x, d4.y)));
+            const float2 y1 = fmul2(make_float2(p[e + 2], p[e + 3]),
+                                    fadd2(make_float2(__uint_as_float(dp[e + 2]), __uint_as_float(dp[e + 3])), make_float2(d4.z, d4.w)));
+            pk[e / 2] = pack_bf16x2(y0.x, y0.y);
+            pk[e / 2 + 1] = pack_bf16x2(y1.x, y1.y);
+          }
+          if (!whole) {
+            // D of a row that holds none may be anything: selected, not scaled
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              pk[e] &= ((seen >> (2 * e)) & 1 ? 0xffffu : 0u) | ((seen >> (2 * e + 1)) & 1 ? 0xffff0000u : 0u);
+          }
+        }
+        tmem_st16(slot_dp(i) + trow, pk);
+        tmem_wait_st();
+        warp_arrive(&ds_full[i & 1], lane);
+      }
+      if (!ok || !mbar_wait(fin, n_seg & 1, &abort_flag, a.dev_err)) break;
+      tc_fence_after();
+      // this warp's columns of dV | dK: D / 2 of the 2 D
+      const bool is_k = w >= 2;
+      const bool direct = s.y0 == 0 && s.y1 == s.n;
+      const float sc = is_k ? rsqrtf(static_cast<float>(D)) : 1.f;
+      const Rows& dst = is_k ? a.dk : a.dv;
+      bf16* out = static_cast<bf16*>(dst.ptr) + s.b * dst.batch + key * dst.token + s.g * dst.head;
+      float* part = a.part + ((static_cast<int64_t>(blockIdx.x) * 2 + (s.y0 == 0 ? 1 : 0)) * kRows + r) * 2 * D;
+      constexpr int kN = D / 2;
+#pragma unroll 1
+      for (int cc = 0; cc < kN; cc += 16) {
+        const int col = (w & 1) * kN + cc;
+        uint32_t v[16];
+        tmem_ld16(tmem + (static_cast<uint32_t>(q4 * 32) << 16) + (is_k ? C::kColK : C::kColV) + col, v);
+        tmem_wait_ld();
+        if (direct) {
+          if (key < a.S) {
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              o[e] = pack_bf16x2(__uint_as_float(v[2 * e]) * sc, __uint_as_float(v[2 * e + 1]) * sc);
+            *reinterpret_cast<uint4*>(out + col) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(out + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<uint4*>(part + (is_k ? D : 0) + col + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+      }
+      warp_arrive(acc_free, lane);
+    }
+  }
+
+  if (abort_flag && warp == 1 && lane == 0) drain_mmas(drain);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Partial sums of the tiles that several CTAs share, in the order of the CTAs.
+// blockIdx.y: 8 rows of the tile.
+template <int D>
+__global__ void __launch_bounds__(256)
+    window_dkv_join_kernel(const __grid_constant__ WindowArgs a, const __grid_constant__ DkvPlan plan) {
+  pdl_enter();
+  const int3 sp = plan.split[blockIdx.x];
+  const int tile = sp.x % plan.n_tiles, bg = sp.x / plan.n_tiles;
+  for (int x = threadIdx.x; x < 8 * 2 * D / 4; x += 256) {
+    const int r = blockIdx.y * 8 + x / (2 * D / 4), col = x % (2 * D / 4) * 4;
+    const int key = tile * kRows + r;
+    if (key >= a.S) return;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = sp.y; c <= sp.z; ++c) {
+      // the first CTA holds the tile's head as its last segment, the others start with it
+      const float4 v = *reinterpret_cast<const float4*>(a.part + ((static_cast<int64_t>(c) * 2 + (c == sp.y ? 1 : 0)) * kRows + r) * 2 * D + col);
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+    const bool is_k = col >= D;
+    const float sc = is_k ? rsqrtf(static_cast<float>(D)) : 1.f;
+    const Rows& dst = is_k ? a.dk : a.dv;
+    bf16* out = static_cast<bf16*>(dst.ptr) + bg / a.Hkv * dst.batch + key * dst.token + bg % a.Hkv * dst.head + (is_k ? col - D : col);
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(sum.x * sc, sum.y * sc), pack_bf16x2(sum.z * sc, sum.w * sc));
+  }
+}
+
+// Share the blocks out evenly; a share holds at least kMinBlocks.
+constexpr int64_t kMinBlocks = 2;
+void make_plan(const WindowArgs& a, DkvPlan* p) {
+  p->pos = 64 / a.G;
+  p->n_tiles = (a.S + kRows - 1) / kRows;
+  const int64_t BH = static_cast<int64_t>(a.B) * a.Hkv;
+  auto blocks = [&](int tile) {
+    const int2 g = dkv_groups(tile, a.S, a.window, a.sinks, p->pos);
+    return static_cast<int64_t>((g.y - g.x) / 2 + 1);
+  };
+  int64_t per = 0;
+  for (int i = 0; i < p->n_tiles; ++i) per += blocks(i);
+  const int64_t total = per * BH;
+  p->n_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sm_count(), kMaxCtas, total / kMinBlocks})));
+  int64_t at = 0;       // blocks of (sequence, kv head) bg before tile x
+  int64_t bg = 0;
+  int x = 0;
+  for (int c = 0; c <= p->n_ctas; ++c) {
+    const int64_t u = total / p->n_ctas * c + std::min<int64_t>(total % p->n_ctas, c);
+    if (u / per != bg) {
+      bg = u / per;
+      at = 0;
+      x = 0;
+    }
+    const int64_t rem = u - bg * per;
+    while (x < p->n_tiles && at + blocks(x) <= rem) at += blocks(x++);
+    p->start[c] = make_int2(static_cast<int>(bg * p->n_tiles + x), static_cast<int>(rem - at));
+  }
+  // a CTA that starts inside a tile continues the one before it
+  p->n_split = 0;
+  for (int c = 1; c < p->n_ctas; ++c) {
+    if (p->start[c].y == 0) continue;
+    int3* last = p->n_split ? &p->split[p->n_split - 1] : nullptr;
+    if (last && last->x == p->start[c].x)
+      last->z = c;
+    else
+      p->split[p->n_split++] = make_int3(p->start[c].x, c - 1, c);
+  }
+}
+
+template <int D>
+cudaError_t launch_bwd(const WindowArgs& a, cudaStream_t stream) {
+  using C = BwdCfg<D>;
+  CUtensorMap tmQ, tmDO, tmK, tmV;
+  const int pos = 64 / a.G;
+  if (!packed_rows_map(&tmQ, a.q, a, pos) || !packed_rows_map(&tmDO, a.dout, a, pos) ||
+      !key_rows_map(&tmK, a.k, a, kRows) || !key_rows_map(&tmV, a.v, a, kRows))
+    return cudaErrorInvalidValue;
+  const int64_t n_tiles = (a.S + 2 * pos - 1) / (2 * pos), grid = n_tiles * a.B * a.Hkv;
+  if (grid > 0x7fffffff || static_cast<int64_t>((a.S + kRows - 1) / kRows) * a.B * a.Hkv > 0x7fffffff)
+    return cudaErrorInvalidConfiguration;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_dq_tc_kernel<D>), static_cast<int>(C::kQSmem));
+  if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(window_dkv_tc_kernel<D>), static_cast<int>(C::kKSmem));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(window_dq_tc_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(kBwdThreads), C::kQSmem, stream, tmQ,
+                 tmDO, tmK, tmV, a, static_cast<int>(n_tiles));
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  DkvPlan plan;
+  make_plan(a, &plan);
+  e = launch_pdl(window_dkv_tc_kernel<D>, dim3(plan.n_ctas), dim3(kBwdThreads), C::kKSmem, stream, tmQ, tmDO, tmK, tmV, a, plan);
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  if (plan.n_split > 0) {
+    e = launch_pdl(window_dkv_join_kernel<D>, dim3(plan.n_split, kRows / 8), dim3(256), 0, stream, a, plan);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t window_bwd_tc_part_floats(int d) { return static_cast<size_t>(kMaxCtas) * 2 * kRows * 2 * d; }
+
+cudaError_t launch_window_bwd_tc(const WindowArgs& a, cudaStream_t stream) {
+  if (a.G > 64) return cudaErrorInvalidValue;
+  switch (a.d) {
+    case 32: return launch_bwd<32>(a, stream);
+    case 64: return launch_bwd<64>(a, stream);
+    case 128: return launch_bwd<128>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace ccgqa

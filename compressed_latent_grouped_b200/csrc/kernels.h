@@ -304,13 +304,16 @@ struct WindowArgs {
   int pos;
   // backward
   Rows dout, dq, dk, dv;
+  float* part;                  // tensor-core path: partial dk, dv sums
   int32_t* dev_err;
   __device__ __forceinline__ int64_t stat_row(int bg, int t, int hl) const {
     return bg * ld + (pos ? static_cast<int64_t>(t / pos) * 64 + t % pos * G : static_cast<int64_t>(t) * G) + hl;
   }
 };
-// bf16, d in {32, 64, 128}, G <= 128: tcgen05.
+// bf16, d in {32, 64, 128}: tcgen05, for G <= 128 (forward) and G <= 64 (backward).
 cudaError_t launch_window_tc(const WindowArgs& a, cudaStream_t stream);
+cudaError_t launch_window_bwd_tc(const WindowArgs& a, cudaStream_t stream);
+size_t window_bwd_tc_part_floats(int d);   // of WindowArgs::part
 template <typename T>
 cudaError_t launch_window_simt(const WindowArgs& a, cudaStream_t stream);
 template <typename T>

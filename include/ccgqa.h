@@ -460,8 +460,10 @@ CCGQA_API size_t ccgqa_window_attention_backward_workspace_size(const ccgqa_conf
 /* Gradients of ccgqa_window_attention: given q, k, v, its out and stats and the
  * gradient dout of out, writes dq, dk, dv (shapes of q, k, v; a kv head's
  * gradient is summed over its G query heads).  Sums in fp32, each gradient
- * rounded once to cfg->dtype; the order of every sum is fixed, so equal
- * calls give equal bits.  dq, dk, dv overlap neither each other nor an
+ * rounded once to cfg->dtype (bf16 with d >= 32 and G <= 64: tcgen05,
+ * probabilities and score gradients rounded to bf16 for the products; otherwise
+ * CUDA cores, fp32); the order of every sum is fixed, so equal calls give equal
+ * bits.  dq, dk, dv overlap neither each other nor an
  * input. */
 CCGQA_API ccgqa_status ccgqa_window_attention_backward(
     const ccgqa_config* cfg, const ccgqa_window* win, const ccgqa_rows* q, const ccgqa_rows* k,
