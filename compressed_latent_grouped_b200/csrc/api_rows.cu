@@ -217,7 +217,7 @@ CCGQA_API size_t ccgqa_cache_attention_workspace_size(const ccgqa_config* cfg, i
                                                       int32_t cap) {
   Geo g;
   if (derive(cfg, &g) != CCGQA_OK || batch <= 0 || cap <= 0) return 0;
-  return attn_workspace(g, batch, cache_attn_splits(attn_units(g, batch), cap));
+  return attn_workspace(g, batch, cache_attn_splits(attn_units(g, batch), cap, kCacheAttnMaxCtas));
 }
 
 CCGQA_API ccgqa_status ccgqa_cache_attention(const ccgqa_config* cfg, const ccgqa_window* win,
@@ -239,7 +239,7 @@ CCGQA_API ccgqa_status ccgqa_cache_attention(const ccgqa_config* cfg, const ccgq
   // the tiles that hold a window and its sinks, at most two partly used each
   const int64_t keys = a.window ? std::min<int64_t>(cache->cap, static_cast<int64_t>(a.window) + a.sinks + 64)
                                 : cache->cap;
-  a.splits = cache_attn_splits(units, keys);
+  a.splits = cache_attn_splits(units, keys, cache_attn_ctas(g.d, c8 ? c8->format : 0, g.G, g.dtype == CCGQA_F32));
   const size_t need = attn_workspace(g, cache->batch, a.splits);
   if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return CCGQA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

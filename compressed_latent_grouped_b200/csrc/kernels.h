@@ -284,8 +284,13 @@ struct CacheAttnArgs {
 constexpr int kCacheAttnHeads = 16, kCacheAttnHeadsF32 = 4;   // query heads of a chunk
 constexpr int kCacheAttnMaxSplits = 256;
 // Splits for `units` (sequence, kv head, chunk)s of at most `keys` visible
-// tokens; does not fall when keys grow.
-int cache_attn_splits(int64_t units, int64_t keys);
+// tokens; does not fall when keys or the CTAs on an SM grow.
+int cache_attn_splits(int64_t units, int64_t keys, int ctas_per_sm);
+constexpr int kCacheAttnMaxCtas = 4;      // on an SM
+// What launch_bounds asks for: registers and shared memory (fp32: registers alone).
+constexpr int cache_attn_ctas(int d, int fmt, int G, bool f32) {
+  return f32 ? 3 : ((d == 128 && fmt == 0) || G > 8 ? 2 : (d == 128 ? 3 : kCacheAttnMaxCtas));
+}
 template <typename T>
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int fmt, cudaStream_t stream);
 
