@@ -319,13 +319,16 @@ def ccgqa_prefill_backward(cfg, weights, x, batch, seq_len, dout, dx, grads, wor
     return st
 
 
+_NO_ROWS = ccgqa_rows(None, 0, 0, 0)
+
+
 def make_rows(t, order="bthd") -> ccgqa_rows:
     """Head rows of a 4-D tensor whose dimensions are batch, token, head and
-    channel in `order` (channels last); None: absent."""
+    channel ("bthd") or batch, head, token and channel ("bhtd"); None: absent."""
     if t is None:
-        return ccgqa_rows(None, 0, 0, 0)
-    st = t.stride()
-    return ccgqa_rows(t.data_ptr(), *(st[order.index(c)] for c in "bth"))
+        return _NO_ROWS
+    b, x, y, _ = t.stride()
+    return ccgqa_rows(t.data_ptr(), b, x, y) if order == "bthd" else ccgqa_rows(t.data_ptr(), b, y, x)
 
 
 def make_cache8(fmt: int, block: int, k_scale, v_scale) -> ccgqa_cache8:

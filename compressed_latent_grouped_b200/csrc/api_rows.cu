@@ -80,8 +80,21 @@ cudaError_t run_append(const Geo& g, const ccgqa_kvcache* c, const ccgqa_cache8*
   x.n_valid = a->n_valid;
   x.pos = a->pos;
   x.rope_on = g.rope_on;
-  if (g.rope_on)
-    for (int i = 0; i < g.d / 2; ++i) x.rope_frac[i] = rope_turn_fraction(g.rope_log2_base, i, g.d);
+  if (g.rope_on) {
+    // the fractions of the last (base, d): 64 powers in extended precision take
+    // longer than the launch
+    static thread_local struct {
+      double log2_base = -1.0;
+      int d = 0;
+      uint64_t frac[64];
+    } last;
+    if (last.log2_base != g.rope_log2_base || last.d != g.d) {
+      for (int i = 0; i < g.d / 2; ++i) last.frac[i] = rope_turn_fraction(g.rope_log2_base, i, g.d);
+      last.log2_base = g.rope_log2_base;
+      last.d = g.d;
+    }
+    std::copy(last.frac, last.frac + g.d / 2, x.rope_frac);
+  }
   x.dev_err = dev_err;
   return launch_append_rope<T>(x, c8 ? c8->format : 0, st);
 }

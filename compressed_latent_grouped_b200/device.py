@@ -159,13 +159,13 @@ def _check(where, name, t, shape, dtype, device, optional=False):
         if optional:
             return
         _bad(where, f"{name} is missing")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         _bad(where, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         _bad(where, f"{name} is {t.dtype}, expected {dtype}")
     if t.device != device:
         _bad(where, f"{name} is on {t.device}, expected {device}")
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if shape[-1] > 1 and t.stride(-1) != 1:
         _bad(where, f"the last dimension of {name} is not contiguous")
 
 
@@ -175,17 +175,32 @@ def _check_dense(where, name, t, shape, dtype, device, optional=False):
         _bad(where, f"{name} is not contiguous")
 
 
-def _workspace(nbytes: int, device, stream):
-    """Scratch of one call, from torch's allocator; handed back to it in the
-    order of the stream the call runs on."""
-    if nbytes == 0:
-        return None
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+class _Call:
+    """The device and stream of one call: ``with _Call(device, stream) as raw``
+    makes the device current and gives the raw stream (the device's current one
+    for None).  Allocations inside come from that stream's pool, so that they go
+    back to it in its order."""
+
+    __slots__ = ("device", "stream", "contexts")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.contexts = device, stream, ()
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.device.index:
+            self.contexts = (torch.cuda.device(self.device),)
+        s = self.stream
+        if s is not None:
+            if isinstance(s, int):
+                s = torch.cuda.ExternalStream(s, device=self.device)
+            self.contexts += (torch.cuda.stream(s),)
+        for c in self.contexts:
+            c.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
 
 
 def head_dim(cfg: B.ccgqa_config) -> int:
@@ -296,14 +311,17 @@ class DeviceKVCache:
         _check(where, "q", q, qs, dt, dev, True)
         _check_dense(where, "n_valid", n_valid, (self.batch,), torch.int32, dev, True)
         _check_dense(where, "pos", pos, (self.batch,), torch.int32, dev, True)
-        with torch.cuda.device(dev):
-            if q is not None and q_out is None:
-                q_out = torch.empty(qs, dtype=dt, device=dev)
-            _check(where, "q_out", q_out, qs, dt, dev, q is None)
-            ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-            a = B.ccgqa_append(B.make_rows(q), B.make_rows(q_out), B.make_rows(k), B.make_rows(v),
-                               B.make_rows(k_out), n, ptr(n_valid), ptr(pos))
-            B.ccgqa_kvcache_append_rope(self.cfg, self.cache, self.cache8, a, self.dev_err, stream)
+        with _Call(dev, stream) as raw:
+            if q is not None:
+                if q_out is None:
+                    q_out = torch.empty(qs, dtype=dt, device=dev)
+                else:
+                    _check(where, "q_out", q_out, qs, dt, dev)
+            rows = B.make_rows
+            a = B.ccgqa_append(rows(q), rows(q_out), rows(k), rows(v), rows(k_out), n,
+                               None if n_valid is None else n_valid.data_ptr(),
+                               None if pos is None else pos.data_ptr())
+            B.ccgqa_kvcache_append_rope(self.cfg, self.cache, self.cache8, a, self.dev_err, raw)
         return q_out
 
     def read(self, first: int, n: int, k_out=None, v_out=None, stream=None):
@@ -311,7 +329,7 @@ class DeviceKVCache:
         [batch, Hkv, n, d]; rows past a sequence's length keep what the output
         held (zeros when allocated here)."""
         shape = (self.batch, self.cfg.n_kv_heads, n, self.d)
-        with torch.cuda.device(self.device):
+        with _Call(self.device, stream) as raw:
             if k_out is None:
                 k_out = torch.zeros(shape, dtype=self.dtype, device=self.device)
             if v_out is None:
@@ -320,7 +338,7 @@ class DeviceKVCache:
             _check("read", "v_out", v_out, shape, self.dtype, self.device)
             B.ccgqa_kvcache_read(self.cfg, self.cache, self.cache8, first, n,
                                  B.make_rows(k_out, "bhtd"), B.make_rows(v_out, "bhtd"), self.dev_err,
-                                 stream)
+                                 raw)
         return k_out, v_out
 
     def attend(self, q, out=None, window: int = 0, sinks: int = 0, stream=None):
@@ -330,13 +348,14 @@ class DeviceKVCache:
         workspace from torch's allocator."""
         shape = (self.batch, self.cfg.n_q_heads, self.d)
         _check_dense("attend", "q", q, shape, self.dtype, self.device)
-        with torch.cuda.device(self.device):
+        with _Call(self.device, stream) as raw:
             if out is None:
                 out = torch.empty(shape, dtype=self.dtype, device=self.device)
-            _check_dense("attend", "out", out, shape, self.dtype, self.device)
-            ws = _workspace(self._attn_ws, self.device, stream)
+            else:
+                _check_dense("attend", "out", out, shape, self.dtype, self.device)
+            ws = None if self._attn_ws == 0 else torch.empty(self._attn_ws, dtype=torch.uint8, device=self.device)
             B.ccgqa_cache_attention(self.cfg, B.ccgqa_window(window, sinks), self.cache, self.cache8, q, out,
-                                    ws, self.dev_err, stream)
+                                    ws, self.dev_err, raw)
         return out
 
     def error_bits(self) -> int:
@@ -365,16 +384,17 @@ def window_attention(cfg, q, k, v, window: int = 0, sinks: int = 0, out=None, wi
     out, or with ``with_stats`` (out, stats), which the backward pass takes."""
     where = "window_attention"
     batch, S, dt, dev, q_shape, _ = _window_inputs(where, cfg, q, k, v)
-    with torch.cuda.device(dev):
+    with _Call(dev, stream) as raw:
         if out is None:
             out = torch.empty(q_shape, dtype=dt, device=dev)
-        _check(where, "out", out, q_shape, dt, dev)
+        else:
+            _check(where, "out", out, q_shape, dt, dev)
         stats = None
         if with_stats:
             stats = torch.empty(B.ccgqa_window_attention_stats_size(cfg, batch, S), dtype=torch.float32, device=dev)
         rows = B.make_rows
         B.ccgqa_window_attention(cfg, B.ccgqa_window(window, sinks), rows(q), rows(k), rows(v), batch, S, rows(out),
-                                 stats, dev_err, stream)
+                                 stats, dev_err, raw)
     return (out, stats) if with_stats else out
 
 
@@ -387,17 +407,18 @@ def window_attention_backward(cfg, q, k, v, out, stats, dout, window: int = 0, s
     _check(where, "out", out, q_shape, dt, dev)
     _check(where, "dout", dout, q_shape, dt, dev)
     _check_dense(where, "stats", stats, (B.ccgqa_window_attention_stats_size(cfg, batch, S),), torch.float32, dev)
-    with torch.cuda.device(dev):
+    _check(where, "dq", dq, q_shape, dt, dev, True)
+    _check(where, "dk", dk, kv_shape, dt, dev, True)
+    _check(where, "dv", dv, kv_shape, dt, dev, True)
+    with _Call(dev, stream) as raw:
         dq, dk, dv = (torch.empty(shape, dtype=dt, device=dev) if x is None else x
                       for x, shape in ((dq, q_shape), (dk, kv_shape), (dv, kv_shape)))
-        _check(where, "dq", dq, q_shape, dt, dev)
-        _check(where, "dk", dk, kv_shape, dt, dev)
-        _check(where, "dv", dv, kv_shape, dt, dev)
-        ws = _workspace(B.ccgqa_window_attention_backward_workspace_size(cfg, batch, S), dev, stream)
+        n = B.ccgqa_window_attention_backward_workspace_size(cfg, batch, S)
+        ws = None if n == 0 else torch.empty(n, dtype=torch.uint8, device=dev)
         rows = B.make_rows
         B.ccgqa_window_attention_backward(cfg, B.ccgqa_window(window, sinks), rows(q), rows(k), rows(v), rows(out),
                                           stats, rows(dout), batch, S, rows(dq), rows(dk), rows(dv), ws, dev_err,
-                                          stream)
+                                          raw)
     return dq, dk, dv
 
 
