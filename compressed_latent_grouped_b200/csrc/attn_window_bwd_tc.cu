@@ -87,19 +87,10 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-// 2^x on 32 values; one pair in four on the FMA pipe.
+// 2^x on 32 values.
 __device__ __forceinline__ void exp2_32(float (&p)[32]) {
 #pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    if (e % 8 == 0) {
-      const float2 y = soft_exp2x2(make_float2(p[e], p[e + 1]));
-      p[e] = y.x;
-      p[e + 1] = y.y;
-    } else {
-      p[e] = fast_exp2(p[e]);
-      p[e + 1] = fast_exp2(p[e + 1]);
-    }
-  }
+  for (int e = 0; e < 32; ++e) p[e] = fast_exp2(p[e]);
 }
 
 // ================================================================ dq pass
@@ -290,8 +281,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         first = sinks - kb;
       }
       if (!row_ok) end = 0;
-      const uint32_t seen = (below32(first) | ~below32(begin)) & below32(end);
-      const bool whole = __all_sync(0xffffffffu, seen == ~0u), none = __all_sync(0xffffffffu, seen == 0u);
+      const bool whole = __all_sync(0xffffffffu, end >= 32 && (begin <= 0 || first >= 32));
+      const bool none = !whole && __all_sync(0xffffffffu, end <= 0 || (begin >= min(end, 32) && first <= 0));
       if (!mbar_wait(&s_full[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err)) {
         ok = false;
         break;
@@ -303,7 +294,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_wait_ld();
       }
       warp_arrive(&s_read[k & 1], lane);
+      // the first half of dP is on its way while the exponentials are formed
+      uint32_t dp0[16];
+      if (!mbar_wait(&dp_full[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
       if (!none) {
+        tmem_ld16(slot_dp(k) + trow, dp0);
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           const float2 y = ffma2(make_float2(p[e], p[e + 1]), c2, nl2);
@@ -312,29 +311,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         exp2_32(p);
         if (!whole) {
+          const uint32_t seen = (below32(first) | ~below32(begin)) & below32(end);
 #pragma unroll
           for (int e = 0; e < 32; ++e) p[e] = (seen >> e) & 1 ? p[e] : 0.f;
         }
       }
-      if (!mbar_wait(&dp_full[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
       uint32_t ds[16];
       if (none) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) ds[e] = 0;
       } else {
-        uint32_t dp[32];
-        tmem_ld32(slot_dp(k) + trow, dp);
+        uint32_t dp1[16];
         tmem_wait_ld();
+        tmem_ld16(slot_dp(k) + trow + 16, dp1);
+        auto grads = [&](const uint32_t (&dp)[16], int at) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 y = fmul2(make_float2(p[2 * e], p[2 * e + 1]),
-                                 fadd2(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), nd2));
-          ds[e] = pack_bf16x2(y.x, y.y);
-        }
+          for (int e = 0; e < 8; ++e) {
+            const float2 y = fmul2(make_float2(p[at + 2 * e], p[at + 2 * e + 1]),
+                                   fadd2(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), nd2));
+            ds[at / 2 + e] = pack_bf16x2(y.x, y.y);
+          }
+        };
+        grads(dp0, 0);
+        tmem_wait_ld();
+        grads(dp1, 16);
       }
       tmem_st16(slot_dp(k) + trow, ds);
       tmem_wait_st();
@@ -580,8 +580,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // rows of the group, here from its row 32 (w & 1): visible in [begin, end)
         const int begin = max(-1, min(key - tg, pos)) * G - (w & 1) * 32;
         const int end = grp > s.g1 ? 0 : max(0, min(stop - tg, pos)) * G - (w & 1) * 32;
-        const uint32_t seen = below32(end) & ~below32(begin);
-        const bool whole = __all_sync(0xffffffffu, seen == ~0u), none = __all_sync(0xffffffffu, seen == 0u);
+        const bool whole = __all_sync(0xffffffffu, begin <= 0 && end >= 32);
+        const bool none = !whole && __all_sync(0xffffffffu, end <= max(begin, 0) || begin >= 32);
+        const uint32_t seen = whole ? ~0u : below32(end) & ~below32(begin);
         const int st = i % C::kRing;
         if (!mbar_wait(&s_full[i & 1], (i >> 1) & 1, &abort_flag, a.dev_err) ||
             !mbar_wait(&q_full[st], (i / C::kRing) & 1, &abort_flag, a.dev_err)) {
