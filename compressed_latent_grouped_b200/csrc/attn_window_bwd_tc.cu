@@ -66,7 +66,7 @@ struct BwdCfg : RowTiles<D> {
   static constexpr uint32_t kColQ = 3 * kRows;                // dq pass: sums
   static constexpr uint32_t kColV = kSlots * kRows, kColK = kColV + D;
   static_assert(kColK + D <= 512 && kColQ + D <= 512, "TMEM columns");
-  static_assert(kQSmem + 1280 <= 227 * 1024 && kKSmem + 256 <= 227 * 1024, "shared memory, with the static part");
+  static_assert(kQSmem + 768 <= 227 * 1024 && kKSmem + 256 <= 227 * 1024, "shared memory, with the static part");
 };
 
 // acc (+)= A B: A 128 x 128 bf16 in TMEM, 32 columns of it at the head of every 32
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint64_t* drain = fin + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ int abort_flag;
-  __shared__ float dpart[2][kRows];
+  __shared__ float dpart[kRows];   // -D
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.G, BH = a.B * a.Hkv;
@@ -243,33 +243,45 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const bool row_ok = u < used && t < a.S;
     const uint32_t trow = (static_cast<uint32_t>(q4 * 32) << 16) + w * 32;
     const int64_t srow = bg * a.ld + static_cast<int64_t>(tile) * kRows + r;
-    float nlse = 0.f, nd = 0.f;   // -lse, -D
+    const float nlse = row_ok ? a.stats[srow] : 0.f;   // -lse
     {
-      // D = rowsum(dO o): two of a row's four warps form one half of it, two the other
-      float acc = 0.f;
-      if (row_ok) {
-        nlse = a.stats[srow];
-        const int h = g * G + hl;
-        const bf16* x = static_cast<const bf16*>(a.dout.ptr) + b * a.dout.batch + t * a.dout.token + h * a.dout.head + (w & 1) * (D / 2);
-        const bf16* y = static_cast<const bf16*>(a.out.ptr) + b * a.out.batch + t * a.out.token + h * a.out.head + (w & 1) * (D / 2);
+      // -D = -rowsum(dO o): D / 8 lanes read a row's 16-byte pieces, so that a warp's
+      // loads cover whole lines (one thread per row took 17000 cycles at d = 128)
+      constexpr int kLanes = D / 8, kStep = 32 / kLanes, kMine = kRows / kSoftWarps;
+      uint4 x4[kMine / kStep], y4[kMine / kStep];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint4 x4 = *reinterpret_cast<const uint4*>(x + i * 8), y4 = *reinterpret_cast<const uint4*>(y + i * 8);
-          const __nv_bfloat162* x2 = reinterpret_cast<const __nv_bfloat162*>(&x4);
-          const __nv_bfloat162* y2 = reinterpret_cast<const __nv_bfloat162*>(&y4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 xf = __bfloat1622float2(x2[e]), yf = __bfloat1622float2(y2[e]);
-            acc = fmaf(xf.x, yf.x, acc);
-            acc = fmaf(xf.y, yf.y, acc);
-          }
+      for (int i = 0; i < kMine / kStep; ++i) {
+        const int rr = (warp - 4) * kMine + i * kStep + lane / kLanes, uu = rr & 63;
+        const int tt = t0 + (rr >> 6) * pos + uu / G, h = g * G + uu % G, e = lane % kLanes * 8;
+        x4[i] = y4[i] = make_uint4(0, 0, 0, 0);
+        if (uu < used && tt < a.S) {
+          x4[i] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.dout.ptr) + b * a.dout.batch + tt * a.dout.token + h * a.dout.head + e);
+          y4[i] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.out.ptr) + b * a.out.batch + tt * a.out.token + h * a.out.head + e);
         }
       }
-      if (w < 2) dpart[w][r] = acc;
+#pragma unroll
+      for (int i = 0; i < kMine / kStep; ++i) {
+        const int rr = (warp - 4) * kMine + i * kStep + lane / kLanes, uu = rr & 63;
+        const __nv_bfloat162* x2 = reinterpret_cast<const __nv_bfloat162*>(&x4[i]);
+        const __nv_bfloat162* y2 = reinterpret_cast<const __nv_bfloat162*>(&y4[i]);
+        float acc = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 xf = __bfloat1622float2(x2[e]), yf = __bfloat1622float2(y2[e]);
+          acc = fmaf(xf.x, yf.x, acc);
+          acc = fmaf(xf.y, yf.y, acc);
+        }
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+        if (lane % kLanes == 0) {
+          dpart[rr] = -acc;
+          if (uu < used && t0 + (rr >> 6) * pos + uu / G < a.S)
+            a.dsum[bg * a.ld + static_cast<int64_t>(tile) * kRows + rr] = -acc;
+        }
+      }
       named_barrier_sync(1, 32 * kSoftWarps);
-      nd = -(dpart[0][r] + dpart[1][r]);
-      if (row_ok && w == 0) a.dsum[srow] = nd;
     }
+    const float nd = dpart[r];
     const float c = kLog2e * rsqrtf(static_cast<float>(D));
     const float2 c2 = make_float2(c, c), nl2 = make_float2(nlse, nlse), nd2 = make_float2(nd, nd);
     bool ok = true;
@@ -349,7 +361,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         uint32_t v[32];
         tmem_ld32(tmem + C::kColQ + trow, v);
         tmem_wait_ld();
-        if (row_ok) store32(dst + w * 32, v, sc);
+        // Q and dO have been read: 2 KB of them per warp
+        warp_store32(row_ok ? dst + w * 32 : nullptr, v, sc, smem + C::kQOffQ + (warp - 4) * 2048, lane);
       }
     }
   }

@@ -47,8 +47,9 @@ struct FwdCfg : RowTiles<D> {
   static constexpr uint32_t kPieceBytes = kPiece * D * 2;     // one K or V piece
   static constexpr uint32_t kPanelQ = 128 * R::kRowBytes;
   static constexpr uint32_t kPanelK = kPiece * R::kRowBytes;
-  static constexpr int kStages = D == 128 ? 4 : (D == 64 ? 6 : 8);
-  static constexpr int kTiles = D == 32 ? 3 : 2;              // S buffers and sums fill TMEM
+  static constexpr int kStages = D == 128 ? 4 : (D == 64 ? 5 : 8);
+  static constexpr int kTiles = D == 64 ? 1 : (D == 32 ? 3 : 2);
+  static constexpr int kCtas = D == 64 ? 2 : 1;               // on an SM
   // one pair in kSoftEvery takes the FMA pipe's exponential (the best shares of
   // the causal kernel, whose softmax this is)
   static constexpr int kSoftEvery = D == 64 ? 3 : (D == 32 ? 5 : 4);
@@ -58,15 +59,15 @@ struct FwdCfg : RowTiles<D> {
   static constexpr uint32_t kOffV = kOffK + kStages * kPieceBytes;
   static constexpr uint32_t kOffBar = kOffV + kStages * kPieceBytes;
   static constexpr size_t kSmem = kOffBar + 512 + 1024;
-  static constexpr uint32_t kTmemCols = 512;
-  static_assert(kTiles * 128 + kTiles * D <= 512, "TMEM columns");
+  static constexpr uint32_t kTmemCols = 512 / kCtas;
+  static_assert(kTiles * 128 + kTiles * D <= 512 / kCtas, "TMEM columns");
   __device__ static constexpr uint32_t col_s(int x, int h) { return x * 128 + h * 64; }
   __device__ static constexpr uint32_t col_p(int x, int h) { return x * 128 + h * 64 + 32; }
   __device__ static constexpr uint32_t col_o(int x) { return kTiles * 128 + x * D; }
 };
 
 template <int D>
-__global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1)
+__global__ void __launch_bounds__(FwdCfg<D>::kThreads, FwdCfg<D>::kCtas)
     window_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WindowArgs a,
                          int n_groups) {
@@ -313,12 +314,13 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, 1)
       const float inv_l = 1.f / l;
       if (a.stats != nullptr && row_ok) a.stats[a.stat_row(bg, t, hl)] = -(m_used + log2f(l));
       bf16* dst = static_cast<bf16*>(a.out.ptr) + b * a.out.batch + t * a.out.token + (g * G + hl) * a.out.head;
+      uint8_t* stage = smem + C::kOffQ + x * C::kTileBytes + q4 * 2048;   // this tile's queries have been read
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         tmem_ld32(trow + C::col_o(x) + c * 32, o);
         tmem_wait_ld();
-        if (row_ok) store32(dst + c * 32, o, inv_l);
+        warp_store32(row_ok ? dst + c * 32 : nullptr, o, inv_l, stage, lane);
       }
     }
   }

@@ -53,16 +53,29 @@ __device__ __forceinline__ uint32_t below32(int n) {
   return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1);
 }
 
-// 32 fp32 values times f as bf16, to 64 contiguous bytes.
-__device__ __forceinline__ void store32(bf16* dst, const uint32_t (&v)[32], float f) {
+// 32 fp32 values times f of each lane's row, as bf16, to 64 contiguous bytes at
+// the lane's dst (null: no store).  The warp turns them in 2 KB of shared memory
+// (16-byte units exchanged against bank conflicts) so that four lanes write a
+// row's 64 bytes: stored straight from their rows, 32 lines a store, a 128 x 128
+// tile took 4000 cycles.
+__device__ __forceinline__ void warp_store32(bf16* dst, const uint32_t (&v)[32], float f, uint8_t* stage, int lane) {
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       w[e] = pack_bf16x2(__uint_as_float(v[u * 8 + 2 * e]) * f, __uint_as_float(v[u * 8 + 2 * e + 1]) * f);
-    *reinterpret_cast<uint4*>(dst + u * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((u ^ (lane >> 1)) & 3) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (lane >> 2), u = lane & 3;
+    const uint4 w = *reinterpret_cast<const uint4*>(stage + row * 64 + ((u ^ (row >> 1)) & 3) * 16);
+    bf16* p = reinterpret_cast<bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
+    if (p != nullptr) *reinterpret_cast<uint4*>(p + u * 8) = w;
+  }
+  __syncwarp();
 }
 
 // Rows of `tiles` tiles of `rows` rows that the packed TMA box does not fill
