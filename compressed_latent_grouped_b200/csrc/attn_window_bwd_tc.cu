@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __shared__ int abort_flag;
   __shared__ float dpart[kRows];   // -D
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int G = a.G, BH = a.B * a.Hkv;
   const int tile = n_tiles - 1 - static_cast<int>(blockIdx.x) / BH;
   const int bg = static_cast<int>(blockIdx.x) % BH;
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tensormap(&tmQ);
       prefetch_tensormap(&tmDO);
       prefetch_tensormap(&tmK);
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc_s = make_idesc_bf16(128, kRows, false), idesc_o = make_idesc_bf16(128, D, true);
       const uint32_t q_base = smem_addr(smem + C::kQOffQ), do_base = smem_addr(smem + C::kQOffDO);
       auto k_base = [&](int k) { return smem_addr(smem + C::kQOffK + k % C::kKStages * C::kTile); };
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   }
 
-  if (abort_flag && warp == 1 && lane == 0) drain_mmas(drain);
+  if (abort_flag && warp == 1 && elect_one()) drain_mmas(drain);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ int abort_flag;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int G = a.G, pos = plan.pos, used = pos * G;
   const int2 from = plan.start[blockIdx.x], to = plan.start[blockIdx.x + 1];
   // the CTA's segments: (tile, blocks [y0, y1) of n)
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // i counts the CTA's blocks over all its segments
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tensormap(&tmQ);
       prefetch_tensormap(&tmDO);
       prefetch_tensormap(&tmK);
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc_s = make_idesc_bf16(128, kRows, false), idesc_o = make_idesc_bf16(128, D, true);
       const uint32_t k_base = smem_addr(smem + C::kKOffK), v_base = smem_addr(smem + C::kKOffV);
       auto q_base = [&](int i) { return smem_addr(smem + C::kKOffQ + i % C::kRing * C::kTile); };
@@ -700,7 +700,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   }
 
-  if (abort_flag && warp == 1 && lane == 0) drain_mmas(drain);
+  if (abort_flag && warp == 1 && elect_one()) drain_mmas(drain);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, FwdCfg<D>::kCtas)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ int abort_flag;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int G = a.G, BH = a.B * a.Hkv;
   const int grp = n_groups - 1 - static_cast<int>(blockIdx.x) / BH;   // the longest first
   const int bg = static_cast<int>(blockIdx.x) % BH;
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, FwdCfg<D>::kCtas)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tensormap(&tmQ);
       prefetch_tensormap(&tmK);
       prefetch_tensormap(&tmV);
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, FwdCfg<D>::kCtas)
     }
   } else if (warp >= 1 && warp <= C::kTiles) {
     // ------------------------------------------------------------ MMA issuers
-    if (lane == 0) {
+    if (elect_one()) {
       const int x = warp - 1;
       const uint32_t idesc_s = make_idesc_bf16(128, kPiece, false);
       const uint32_t idesc_o = make_idesc_bf16(128, D, true);
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, FwdCfg<D>::kCtas)
     }
   }
 
-  if (abort_flag && warp >= 1 && warp <= C::kTiles && lane == 0) drain_mmas(drain);
+  if (abort_flag && warp >= 1 && warp <= C::kTiles && elect_one()) drain_mmas(drain);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

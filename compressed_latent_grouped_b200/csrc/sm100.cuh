@@ -99,6 +99,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// One lane of a converged warp, the same one every time.  Where the branch that
+// leads to it is also uniform for the compiler (warp_index), the operands of the
+// instructions inside are formed in uniform registers; behind a test of the lane
+// number each has to be moved there first, which made a tcgen05.mma cost its
+// issuing thread about 100 cycles.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
+
 // ---------------------------------------------------------------- TMA
 // Bring the 128-byte line holding p into L2 (no register result, no wait).
 __device__ __forceinline__ void prefetch_l2(const void* p) {
