@@ -62,9 +62,8 @@ struct BwdCfg : RowTiles<D> {
   static constexpr uint32_t kKOffD = kKOffL + kRing * kRows * 4;
   static constexpr uint32_t kKOffBar = kKOffD + kRing * kRows * 4;
   static constexpr size_t kKSmem = kKOffBar + 512 + 1024;
-  static constexpr int kSlots = D == 128 ? 2 : 3;             // dkv pass
   static constexpr uint32_t kColQ = 3 * kRows;                // dq pass: sums
-  static constexpr uint32_t kColV = kSlots * kRows, kColK = kColV + D;
+  static constexpr uint32_t kColV = 2 * kRows, kColK = kColV + D;
   static_assert(kColK + D <= 512 && kColQ + D <= 512, "TMEM columns");
   static_assert(kQSmem + 768 <= 227 * 1024 && kKSmem + 256 <= 227 * 1024, "shared memory, with the static part");
 };
@@ -78,6 +77,20 @@ __device__ __forceinline__ void mma_slot_by_rows(uint32_t acc, uint32_t slot, ui
   for (int k = 0; k < kRows / 16; ++k)
     mma_ts(acc, slot + (k >> 1) * 32 + (k & 1) * 8,
            make_smem_desc(b_base + k * 16 * C::kRowBytes, C::kPanel, C::kSbo, C::kSwz), idesc, !first || k > 0 ? 1u : 0u);
+}
+
+// acc (+)= A B over half h of a block: A 128 x 64 bf16 in TMEM, 32 columns of it at
+// the head of every 32 TMEM columns of the half; B the half's 64 rows of the tile
+// at b_base, read MN-major.
+template <int D>
+__device__ __forceinline__ void mma_half_by_rows(uint32_t acc, uint32_t slot, uint32_t b_base, int h, uint32_t idesc,
+                                                 bool first) {
+  using C = BwdCfg<D>;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    mma_ts(acc, slot + h * 64 + (k >> 1) * 32 + (k & 1) * 8,
+           make_smem_desc(b_base + (h * 64 + k * 16) * C::kRowBytes, C::kPanel, C::kSbo, C::kSwz), idesc,
+           !first || k > 0 ? 1u : 0u);
 }
 
 // Arrival of a warp whose TMEM accesses have completed.
@@ -408,12 +421,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint64_t* q_empty = q_full + C::kRing;         // [kRing] dK issued, and lse read by every warp
   uint64_t* do_full = q_empty + C::kRing;        // [kRing] dO and D
   uint64_t* do_empty = do_full + C::kRing;
-  uint64_t* s_full = do_empty + C::kRing;        // [2], by block
-  uint64_t* dp_full = s_full + 2;                // [2]
-  uint64_t* p_full = dp_full + 2;                // [2], one arrival per warp
-  uint64_t* ds_full = p_full + 2;                // [2], one arrival per warp
-  uint64_t* out_done = ds_full + 2;              // the issuer's own: dV or dK complete
-  uint64_t* fin = out_done + 1;                  // a segment's sums complete
+  uint64_t* s_full = do_empty + C::kRing;        // [half]
+  uint64_t* dp_full = s_full + 2;                // [half]
+  uint64_t* p_full = dp_full + 2;                // [half], one arrival per warp
+  uint64_t* ds_full = p_full + 2;                // [half], one arrival per warp
+  uint64_t* dv_done = ds_full + 2;               // [half]
+  uint64_t* dk_done = dv_done + 2;               // [half]
+  uint64_t* fin = dk_done + 2;                   // a segment's sums complete
   uint64_t* acc_free = fin + 1;                  // its sums read, one arrival per warp
   uint64_t* drain = acc_free + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -454,10 +468,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&dp_full[i], 1);
-      mbar_init(&p_full[i], kSoftWarps);
-      mbar_init(&ds_full[i], kSoftWarps);
+      mbar_init(&p_full[i], kSoftWarps / 2);
+      mbar_init(&ds_full[i], kSoftWarps / 2);
+      mbar_init(&dv_done[i], 1);
+      mbar_init(&dk_done[i], 1);
     }
-    mbar_init(out_done, 1);
     mbar_init(fin, 1);
     mbar_init(acc_free, kSoftWarps);
     mbar_init(drain, 1);
@@ -473,8 +488,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto slot_s = [&](int i) { return tmem + static_cast<uint32_t>(C::kSlots == 3 ? 2 * i % 3 : 0) * kRows; };
-  auto slot_dp = [&](int i) { return tmem + static_cast<uint32_t>(C::kSlots == 3 ? (2 * i + 1) % 3 : 1) * kRows; };
+  const uint32_t slot_s = tmem, slot_dp = tmem + kRows;
 
   // i counts the CTA's blocks over all its segments
   if (warp == 0) {
@@ -523,59 +537,84 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (elect_one()) {
-      const uint32_t idesc_s = make_idesc_bf16(128, kRows, false), idesc_o = make_idesc_bf16(128, D, true);
+      const uint32_t idesc_s = make_idesc_bf16(128, 64, false), idesc_o = make_idesc_bf16(128, D, true);
       const uint32_t k_base = smem_addr(smem + C::kKOffK), v_base = smem_addr(smem + C::kKOffV);
       auto q_base = [&](int i) { return smem_addr(smem + C::kKOffQ + i % C::kRing * C::kTile); };
       auto do_base = [&](int i) { return smem_addr(smem + C::kKOffDO + i % C::kRing * C::kTile); };
-      auto issue_s = [&](int i) {
-        if (!mbar_wait(&q_full[i % C::kRing], (i / C::kRing) & 1, &abort_flag, a.dev_err)) return false;
+      auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, &abort_flag, a.dev_err); };
+      auto issue_s = [&](int i, int h) {
         tc_fence_after();
-        mma_rows_by_rows<D>(slot_s(i), k_base, C::kPanel, q_base(i), C::kPanel, idesc_s);
-        mma_commit(&s_full[i & 1]);
-        return true;
+        mma_rows_by_rows<D>(slot_s + h * 64, k_base, C::kPanel, q_base(i) + h * 64 * C::kRowBytes, C::kPanel, idesc_s);
+        mma_commit(&s_full[h]);
       };
-      auto issue_dp = [&](int i) {
-        if (!mbar_wait(&do_full[i % C::kRing], (i / C::kRing) & 1, &abort_flag, a.dev_err)) return false;
+      auto issue_dp = [&](int i, int h) {
         tc_fence_after();
-        mma_rows_by_rows<D>(slot_dp(i), v_base, C::kPanel, do_base(i), C::kPanel, idesc_s);
-        mma_commit(&dp_full[i & 1]);
-        return true;
+        mma_rows_by_rows<D>(slot_dp + h * 64, v_base, C::kPanel, do_base(i) + h * 64 * C::kRowBytes, C::kPanel, idesc_s);
+        mma_commit(&dp_full[h]);
       };
-      int i = 0, n_seg = 0, outs = 0;   // outs: completions of out_done waited for
+      auto issue_dv = [&](int i, int h, bool first) {
+        tc_fence_after();
+        mma_half_by_rows<D>(tmem + C::kColV, slot_s, do_base(i), h, idesc_o, first);
+        mma_commit(&dv_done[h]);
+      };
+      auto issue_dk = [&](int i, int h, bool first) {
+        tc_fence_after();
+        mma_half_by_rows<D>(tmem + C::kColK, slot_dp, q_base(i), h, idesc_o, first);
+        mma_commit(&dk_done[h]);
+      };
+      int i = 0, n_seg = 0;
       bool ok = true;
       Seg s;
       for (int x = from.x; ok && segment(x, &s); ++x, ++n_seg) {
         const int i0 = i, i1 = i + s.y1 - s.y0;
-        ok = (n_seg == 0 || mbar_wait(acc_free, (n_seg - 1) & 1, &abort_flag, a.dev_err)) &&
-             mbar_wait(kv_full, n_seg & 1, &abort_flag, a.dev_err) && issue_s(i) && issue_dp(i) &&
-             (C::kSlots == 2 || i + 1 >= i1 || issue_s(i + 1));
+        ok = (n_seg == 0 || wait(acc_free, n_seg - 1)) && wait(kv_full, n_seg) && wait(&q_full[i % C::kRing], i / C::kRing);
+        if (!ok) break;
+        issue_s(i, 0);
+        issue_s(i, 1);
+        if (!(ok = wait(&do_full[i % C::kRing], i / C::kRing))) break;
+        issue_dp(i, 0);
+        issue_dp(i, 1);
+        // A half's next scores take its slot once the product before has read it.
+        // That wait comes one event later than the product's issue: the halves'
+        // events alternate, and the tensor core has the other half's work meanwhile.
         for (; ok && i < i1; ++i) {
-          if (!(ok = mbar_wait(&p_full[i & 1], (i >> 1) & 1, &abort_flag, a.dev_err))) break;
-          tc_fence_after();
-          mma_slot_by_rows<D>(tmem + C::kColV, slot_s(i), do_base(i), idesc_o, i == i0);
-          mma_commit(out_done);
-          // P's slot, once dV has read it: dP(i + 1), or with two slots S(i + 1)
-          if (!(ok = mbar_wait(out_done, outs++ & 1, &abort_flag, a.dev_err))) break;
-          if (i + 1 < i1 && !(ok = C::kSlots == 3 ? issue_dp(i + 1) : issue_s(i + 1))) break;
-          if (!(ok = mbar_wait(&ds_full[i & 1], (i >> 1) & 1, &abort_flag, a.dev_err))) break;
-          tc_fence_after();
-          // dV and every score have read dO(i); D(i) has been read before ds_full
+          const bool more = i + 1 < i1;
+          if (!(ok = wait(&p_full[0], i))) break;
+          issue_dv(i, 0, i == i0);
+          if (i > i0) {
+            if (!(ok = wait(&dk_done[1], i - 1))) break;
+            issue_dp(i, 1);
+          }
+          if (!(ok = wait(&p_full[1], i))) break;
+          issue_dv(i, 1, false);
+          if (more) {
+            if (!(ok = wait(&dv_done[0], i) && wait(&q_full[(i + 1) % C::kRing], (i + 1) / C::kRing))) break;
+            issue_s(i + 1, 0);
+          }
+          if (!(ok = wait(&ds_full[0], i))) break;
+          issue_dk(i, 0, i == i0);
+          if (more) {
+            if (!(ok = wait(&dv_done[1], i))) break;
+            issue_s(i + 1, 1);
+          }
+          if (!(ok = wait(&ds_full[1], i))) break;
+          // dV and every score have read dO(i); lse(i) and D(i) have been read
           mma_commit(&do_empty[i % C::kRing]);
-          mma_slot_by_rows<D>(tmem + C::kColK, slot_dp(i), q_base(i), idesc_o, i == i0);
-          mma_commit(out_done);
+          issue_dk(i, 1, false);
           mma_commit(&q_empty[i % C::kRing]);
-          if (i + 1 == i1) {
+          if (!more) {
             mma_commit(fin);
             mma_commit(kv_empty);
+          } else {
+            if (!(ok = wait(&dk_done[0], i) && wait(&do_full[(i + 1) % C::kRing], (i + 1) / C::kRing))) break;
+            issue_dp(i + 1, 0);
           }
-          if (!(ok = mbar_wait(out_done, outs++ & 1, &abort_flag, a.dev_err))) break;
-          if (C::kSlots == 3 ? i + 2 < i1 && !(ok = issue_s(i + 2)) : i + 1 < i1 && !(ok = issue_dp(i + 1))) break;
         }
       }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ scores
-    const int w = (warp - 4) >> 2, q4 = warp & 3;
+    const int w = (warp - 4) >> 2, q4 = warp & 3, half = w >> 1;
     const int r = q4 * 32 + lane;                 // key row == TMEM lane
     const uint32_t trow = (static_cast<uint32_t>(q4 * 32) << 16) + w * 32;
     const float c = kLog2e * rsqrtf(static_cast<float>(D));
@@ -588,7 +627,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // positions [key, stop) see the key
       const int stop = key >= a.S ? 0 : (key < a.sinks ? a.S : static_cast<int>(min(static_cast<int64_t>(a.S), static_cast<int64_t>(key) + a.window)));
       for (int y = s.y0; y < s.y1; ++y, ++i) {
-        const int grp = s.g0 + 2 * y + (w >> 1);
+        const int grp = s.g0 + 2 * y + half;
         const int tg = min(grp, s.g1 + 1) * pos;   // a group past the last one: no position is left
         // rows of the group, here from its row 32 (w & 1): visible in [begin, end)
         const int begin = max(-1, min(key - tg, pos)) * G - (w & 1) * 32;
@@ -597,7 +636,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const bool none = !whole && __all_sync(0xffffffffu, end <= max(begin, 0) || begin >= 32);
         const uint32_t seen = whole ? ~0u : below32(end) & ~below32(begin);
         const int st = i % C::kRing;
-        if (!mbar_wait(&s_full[i & 1], (i >> 1) & 1, &abort_flag, a.dev_err) ||
+        if (!mbar_wait(&s_full[half], i & 1, &abort_flag, a.dev_err) ||
             !mbar_wait(&q_full[st], (i / C::kRing) & 1, &abort_flag, a.dev_err)) {
           ok = false;
           break;
@@ -609,7 +648,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) pk[e] = 0;
         } else {
-          tmem_ld32(slot_s(i) + trow, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
+          tmem_ld32(slot_s + trow, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
           const float4* nl = reinterpret_cast<const float4*>(smem + C::kKOffL + st * kRows * 4) + w * 8;
           tmem_wait_ld();
 #pragma unroll
@@ -630,10 +669,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(p[2 * e], p[2 * e + 1]);
         }
-        tmem_st16(slot_s(i) + trow, pk);
+        tmem_st16(slot_s + trow, pk);
         tmem_wait_st();
-        warp_arrive(&p_full[i & 1], lane);
-        if (!mbar_wait(&dp_full[i & 1], (i >> 1) & 1, &abort_flag, a.dev_err) ||
+        warp_arrive(&p_full[half], lane);
+        if (!mbar_wait(&dp_full[half], i & 1, &abort_flag, a.dev_err) ||
             !mbar_wait(&do_full[st], (i / C::kRing) & 1, &abort_flag, a.dev_err)) {
           ok = false;
           break;
@@ -641,7 +680,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_after();
         if (!none) {
           uint32_t dp[32];
-          tmem_ld32(slot_dp(i) + trow, dp);
+          tmem_ld32(slot_dp + trow, dp);
           const float4* nd = reinterpret_cast<const float4*>(smem + C::kKOffD + st * kRows * 4) + w * 8;
           tmem_wait_ld();
 #pragma unroll
@@ -661,9 +700,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               pk[e] &= ((seen >> (2 * e)) & 1 ? 0xffffu : 0u) | ((seen >> (2 * e + 1)) & 1 ? 0xffff0000u : 0u);
           }
         }
-        tmem_st16(slot_dp(i) + trow, pk);
+        tmem_st16(slot_dp + trow, pk);
         tmem_wait_st();
-        warp_arrive(&ds_full[i & 1], lane);
+        warp_arrive(&ds_full[half], lane);
       }
       if (!ok || !mbar_wait(fin, n_seg & 1, &abort_flag, a.dev_err)) break;
       tc_fence_after();
