@@ -143,12 +143,32 @@ bool window_args(const Geo& g, const ccgqa_window* win, int B, int S, const ccgq
 }
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255) == 0; }
 bool window_tc(const Geo& g, int max_group) { return g.dtype == CCGQA_BF16 && g.d >= 32 && g.G <= max_group; }
-// dsum, then the tensor-core path's partial sums.
+// Statistics: a float per row, then a second one, or (tensor-core backward pass)
+// what rounding took from out, in bf16.
+int64_t stats_floats(const Geo& g, int64_t B, int64_t S) {
+  const int64_t rows = B * g.Hkv * stat_rows(g, S);
+  return rows + (window_tc(g, 64) ? B * S * g.Hq * g.d / 2 : rows);
+}
+void set_stats(const Geo& g, float* stats, WindowArgs* a) {
+  a->stats = stats;
+  if (!stats) return;
+  float* second = stats + static_cast<int64_t>(a->B) * g.Hkv * a->ld;
+  if (window_tc(g, 64))
+    a->o_lo = reinterpret_cast<bf16*>(second);
+  else
+    a->inv_l = second;
+}
+// dsum, then the partial sums of dk and dv.
 size_t window_dsum_bytes(const Geo& g, int64_t B, int64_t S) {
   return up256(static_cast<size_t>(B * g.Hkv * stat_rows(g, S)) * sizeof(float));
 }
 size_t window_bwd_workspace(const Geo& g, int64_t B, int64_t S) {
-  return window_dsum_bytes(g, B, S) + (window_tc(g, 64) ? window_bwd_tc_part_floats(g.d) * sizeof(float) : 0);
+  size_t part = window_bwd_tc_part_floats(g.d);
+  if (!window_tc(g, 64)) {
+    const int parts = window_bwd_simt_parts(B, S, g.Hkv, g.G, g.d);
+    part = parts > 1 ? static_cast<size_t>(parts) * B * S * g.Hkv * 2 * g.d : 0;
+  }
+  return window_dsum_bytes(g, B, S) + part * sizeof(float);
 }
 
 bool window_ok(const ccgqa_window* w) { return !w || (w->window >= 0 && w->sinks >= 0); }
@@ -287,7 +307,7 @@ CCGQA_API size_t ccgqa_window_attention_stats_size(const ccgqa_config* cfg, int3
                                                    int32_t seq_len) {
   Geo g;
   if (derive(cfg, &g) != CCGQA_OK || batch <= 0 || seq_len <= 0) return 0;
-  return static_cast<size_t>(static_cast<int64_t>(batch) * g.Hkv * stat_rows(g, seq_len));
+  return static_cast<size_t>(stats_floats(g, batch, seq_len));
 }
 
 CCGQA_API ccgqa_status ccgqa_window_attention(const ccgqa_config* cfg, const ccgqa_window* win,
@@ -303,7 +323,7 @@ CCGQA_API ccgqa_status ccgqa_window_attention(const ccgqa_config* cfg, const ccg
   if (batch == 0 || seq_len == 0) return CCGQA_OK;
   WindowArgs a;
   if (!window_args(g, win, batch, seq_len, q, k, v, out, dev_err, &a)) return CCGQA_ERR_INVALID_ARG;
-  a.stats = stats;
+  set_stats(g, stats, &a);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!stream_allowed(st)) return CCGQA_ERR_INVALID_ARG;
   const cudaError_t e = window_tc(g, 128)          ? launch_window_tc(a, st)
@@ -341,13 +361,14 @@ CCGQA_API ccgqa_status ccgqa_window_attention_backward(
     return CCGQA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!stream_allowed(st)) return CCGQA_ERR_INVALID_ARG;
-  a.stats = const_cast<float*>(stats);
+  set_stats(g, const_cast<float*>(stats), &a);
   a.dsum = static_cast<float*>(workspace);
   a.dout = rows_of(*dout, batch, seq_len, g.Hq);
   a.dq = rows_of(*dq, batch, seq_len, g.Hq);
   a.dk = rows_of(*dk, batch, seq_len, g.Hkv);
   a.dv = rows_of(*dv, batch, seq_len, g.Hkv);
   a.part = a.dsum + window_dsum_bytes(g, batch, seq_len) / sizeof(float);
+  a.parts = window_bwd_simt_parts(batch, seq_len, g.Hkv, g.G, g.d);
   const cudaError_t e = window_tc(g, 64)           ? launch_window_bwd_tc(a, st)
                         : g.dtype == CCGQA_BF16 ? launch_window_bwd_simt<bf16>(a, st)
                                                 : launch_window_bwd_simt<float>(a, st);

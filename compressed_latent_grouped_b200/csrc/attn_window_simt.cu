@@ -13,9 +13,13 @@
 // shared memory as fp32 rows padded by 16 bytes, so that 8 neighbouring rows'
 // 16-byte reads fall into different banks; 64 fused multiply-adds per 8 reads of
 // 16 bytes.  Only tiles with a visible pair are visited.  The bound is the FMA
-// pipe.  dk and dv of a key tile belong to one CTA, which walks the group's
-// heads and the query tiles that see it, so nothing is added by atomics and
-// equal calls give equal bits.
+// pipe.  The (head, query tile) pairs of a key tile are shared out to as many CTAs
+// as fill the GPU; their partial dk and dv, fp32, are added by a second kernel in
+// the order of the pairs, so equal calls give equal bits.  Each tile's products are
+// summed by themselves before they join the running sums, which keeps the error
+// of long sums near that of one tile.
+#include <algorithm>
+
 #include "kernels.h"
 
 namespace ccgqa {
@@ -93,8 +97,9 @@ __device__ __forceinline__ void dot_tile(const float* a, const float* b, int ty,
 // o[i][n] += sum_k w[ty 4 + i][k] b[k][col n]   (kTrans: w[k][ty 4 + i])
 template <int D, bool kTrans>
 __device__ __forceinline__ void mix_tile(const float* w, const float* b, int ty, int tx,
-                                         float (&o)[4][SimtCfg<D>::kCols]) {
+                                         float (&sum)[4][SimtCfg<D>::kCols]) {
   using C = SimtCfg<D>;
+  float o[4][C::kCols] = {};
 #pragma unroll 2
   for (int k = 0; k < kT; k += 4) {
     float x[4][4];   // kTrans: [k][i], else [i][k]
@@ -114,6 +119,10 @@ __device__ __forceinline__ void mix_tile(const float* w, const float* b, int ty,
             o[i][n + v] = fmaf(kTrans ? x[u][i] : x[i][u], y[v], o[i][n + v]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int n = 0; n < C::kCols; ++n) sum[i][n] += o[i][n];
 }
 
 __device__ __forceinline__ bool sees(int t, int s, int window, int sinks) {
@@ -212,16 +221,21 @@ __global__ void __launch_bounds__(kThreads)
     for (int off = 8; off > 0; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
     f[i] = 1.f / l[i];
     const int t = t0 + ty * 4 + i;
-    if (a.stats && t < a.S && tx == 0) a.stats[a.stat_row(b * a.Hkv + g, t, h - g * a.G)] = -(m[i] + log2f(l[i]));
+    if (a.stats && t < a.S && tx == 0) {
+      const int64_t at = a.stat_row(b * a.Hkv + g, t, h - g * a.G);
+      a.stats[at] = -m[i];
+      a.inv_l[at] = f[i];
+    }
   }
   store_rows<T, D>(a.out, b, t0, h, a.S, ty, tx, o, f);
 }
 
-// p and dS of a tile, into shared memory.  L, Ds: -lse and -D of this thread's rows.
+// p and dS of a tile, into shared memory.  M, L, Ds: -m, 1 / l and -D of this
+// thread's rows.
 template <int D>
 __device__ __forceinline__ void score_grads(const WindowArgs& a, const float* Q, const float* dO, const float* K,
                                             const float* V, float* P, float* dS, int t0, int s0, int ty, int tx,
-                                            const float (&L)[4], const float (&Ds)[4], float c) {
+                                            const float (&M)[4], const float (&L)[4], const float (&Ds)[4], float c) {
   float s[4][4] = {}, e[4][4] = {};
   dot_tile<D>(Q, K, ty, tx, s);
   dot_tile<D>(dO, V, ty, tx, e);
@@ -231,7 +245,7 @@ __device__ __forceinline__ void score_grads(const WindowArgs& a, const float* Q,
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int k = s0 + tx + 16 * j;
-      const float p = t < a.S && sees(t, k, a.window, a.sinks) ? exp2f(fmaf(s[i][j], c, L[i])) : 0.f;
+      const float p = t < a.S && sees(t, k, a.window, a.sinks) ? exp2f(fmaf(s[i][j], c, M[i])) * L[i] : 0.f;
       if (P) P[(ty * 4 + i) * kPs + tx + 16 * j] = p;
       dS[(ty * 4 + i) * kPs + tx + 16 * j] = p == 0.f ? 0.f : p * (e[i][j] + Ds[i]);
     }
@@ -254,7 +268,7 @@ __global__ void __launch_bounds__(kThreads)
   load_tile<T, D>(dO, a.dout, b, t0, h, a.S);
   load_tile<T, D>(K, a.out, b, t0, h, a.S);   // o, for D
   __syncthreads();
-  float L[4], Ds[4];
+  float M[4], L[4], Ds[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = ty * 4 + i, t = t0 + row;
@@ -263,10 +277,11 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
     Ds[i] = -x;
-    L[i] = 0.f;
+    M[i] = L[i] = 0.f;
     if (t < a.S) {
       const int64_t at = a.stat_row(b * a.Hkv + g, t, h - g * a.G);
-      L[i] = a.stats[at];
+      M[i] = a.stats[at];
+      L[i] = a.inv_l[at];
       if (tx == 0) a.dsum[at] = -x;
     }
   }
@@ -279,7 +294,7 @@ __global__ void __launch_bounds__(kThreads)
     load_tile<T, D>(K, a.k, b, s0, g, a.S);
     load_tile<T, D>(V, a.v, b, s0, g, a.S);
     __syncthreads();
-    score_grads<D>(a, Q, dO, K, V, nullptr, dS, t0, s0, ty, tx, L, Ds, c);
+    score_grads<D>(a, Q, dO, K, V, nullptr, dS, t0, s0, ty, tx, M, L, Ds, c);
     __syncwarp();
     mix_tile<D, false>(dS, K, ty, tx, o);
   }
@@ -298,40 +313,87 @@ __global__ void __launch_bounds__(kThreads)
   float *P = V + kT * C::kLd, *dS = P + kT * kPs;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   const int tiles = (a.S + kT - 1) / kT;
-  const int s0 = static_cast<int>(blockIdx.x) % tiles * kT;   // the sinks' tile, the longest, starts first
-  const int g = static_cast<int>(blockIdx.x) / tiles % a.Hkv, b = static_cast<int>(blockIdx.x) / tiles / a.Hkv;
+  int x = blockIdx.x;
+  const int part = x % a.parts;
+  x /= a.parts;
+  const int s0 = x % tiles * kT;
+  const int g = x / tiles % a.Hkv, b = x / tiles / a.Hkv;
   load_tile<T, D>(K, a.k, b, s0, g, a.S);
   load_tile<T, D>(V, a.v, b, s0, g, a.S);
-  // queries up to t_end see a key of the tile
+  // queries up to t_end see a key of the tile; the pairs (head, query tile), in
+  // order, are cut into a.parts shares
   const int64_t reach = static_cast<int64_t>(s0) + kT - 1 + a.window;
   const int t_end = s0 < a.sinks || reach > a.S ? a.S : static_cast<int>(reach);
+  const int per = (t_end - s0 + kT - 1) / kT;
+  const int64_t pairs = static_cast<int64_t>(per) * a.G;
+  const int64_t first = pairs * part / a.parts, last = pairs * (part + 1) / a.parts;
   float dk[4][C::kCols] = {}, dv[4][C::kCols] = {};
   const float c = kLog2eW * rsqrtf(static_cast<float>(D));
-  for (int hl = 0; hl < a.G; ++hl) {
-    const int h = g * a.G + hl;
-    for (int t0 = s0; t0 < t_end; t0 += kT) {
-      __syncthreads();
-      load_tile<T, D>(Q, a.q, b, t0, h, a.S);
-      load_tile<T, D>(dO, a.dout, b, t0, h, a.S);
-      float L[4], Ds[4];
+  for (int64_t u = first; u < last; ++u) {
+    const int hl = static_cast<int>(u / per), h = g * a.G + hl;
+    const int t0 = s0 + static_cast<int>(u % per) * kT;
+    __syncthreads();
+    load_tile<T, D>(Q, a.q, b, t0, h, a.S);
+    load_tile<T, D>(dO, a.dout, b, t0, h, a.S);
+    float M[4], L[4], Ds[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = t0 + ty * 4 + i;
-        const int64_t at = a.stat_row(b * a.Hkv + g, min(t, a.S - 1), hl);
-        L[i] = a.stats[at];
-        Ds[i] = a.dsum[at];
-      }
-      __syncthreads();
-      score_grads<D>(a, Q, dO, K, V, P, dS, t0, s0, ty, tx, L, Ds, c);
-      __syncthreads();
-      mix_tile<D, true>(P, dO, ty, tx, dv);
-      mix_tile<D, true>(dS, Q, ty, tx, dk);
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + ty * 4 + i;
+      const int64_t at = a.stat_row(b * a.Hkv + g, min(t, a.S - 1), hl);
+      M[i] = a.stats[at];
+      L[i] = a.inv_l[at];
+      Ds[i] = a.dsum[at];
     }
+    __syncthreads();
+    score_grads<D>(a, Q, dO, K, V, P, dS, t0, s0, ty, tx, M, L, Ds, c);
+    __syncthreads();
+    mix_tile<D, true>(P, dO, ty, tx, dv);
+    mix_tile<D, true>(dS, Q, ty, tx, dk);
   }
   const float inv = rsqrtf(static_cast<float>(D));
-  const float fk[4] = {inv, inv, inv, inv}, fv[4] = {1.f, 1.f, 1.f, 1.f};
-  store_rows<T, D>(a.dk, b, s0, g, a.S, ty, tx, dk, fk);
-  store_rows<T, D>(a.dv, b, s0, g, a.S, ty, tx, dv, fv);
+  if (a.parts == 1) {
+    const float fk[4] = {inv, inv, inv, inv}, fv[4] = {1.f, 1.f, 1.f, 1.f};
+    store_rows<T, D>(a.dk, b, s0, g, a.S, ty, tx, dk, fk);
+    store_rows<T, D>(a.dv, b, s0, g, a.S, ty, tx, dv, fv);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = s0 + ty * 4 + i;
+    if (t >= a.S) continue;
+    float* row = a.part + (((static_cast<int64_t>(part) * a.B + b) * a.S + t) * a.Hkv + g) * 2 * D;
+#pragma unroll
+    for (int n = 0; n < C::kCols; ++n) {
+      row[C::col(tx, n)] = dk[i][n] * inv;
+      row[D + C::col(tx, n)] = dv[i][n];
+    }
+  }
+}
+
+// dk and dv from their parts.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) window_dkv_sum_kernel(const __grid_constant__ WindowArgs a, int64_t n) {
+  pdl_enter();
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;   // four channels of dk or dv
+  if (x >= n) return;
+  const int w = 2 * a.d / 4;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = 0; p < a.parts; ++p) {
+    const float4 v = reinterpret_cast<const float4*>(a.part)[p * n + x];
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  }
+  const int64_t row = x / w;
+  const int e = static_cast<int>(x % w) * 4;
+  const int g = static_cast<int>(row % a.Hkv), t = static_cast<int>(row / a.Hkv % a.S), b = static_cast<int>(row / a.Hkv / a.S);
+  const Rows& r = e < a.d ? a.dk : a.dv;
+  T* out = static_cast<T*>(r.ptr) + b * r.batch + t * r.token + g * r.head + (e < a.d ? e : e - a.d);
+  out[0] = from_f32<T>(sum.x);
+  out[1] = from_f32<T>(sum.y);
+  out[2] = from_f32<T>(sum.z);
+  out[3] = from_f32<T>(sum.w);
 }
 
 template <typename Kernel>
@@ -357,10 +419,26 @@ cudaError_t bwd_d(const WindowArgs& a, cudaStream_t stream) {
   const int64_t tiles = (a.S + kT - 1) / kT;
   const cudaError_t e = launch_one(window_dq_simt_kernel<T, D>, tiles * a.Hq * a.B, 4 * C::kTileBytes + C::kPBytes, a, stream);
   if (e != cudaSuccess) return e;
-  return launch_one(window_dkv_simt_kernel<T, D>, tiles * a.Hkv * a.B, 4 * C::kTileBytes + 2 * C::kPBytes, a, stream);
+  const cudaError_t k = launch_one(window_dkv_simt_kernel<T, D>, tiles * a.Hkv * a.B * a.parts,
+                                   4 * C::kTileBytes + 2 * C::kPBytes, a, stream);
+  if (k != cudaSuccess || a.parts == 1) return k;
+  const int64_t n = static_cast<int64_t>(a.B) * a.S * a.Hkv * 2 * D / 4;
+  const cudaError_t j = launch_pdl(window_dkv_sum_kernel<T>, dim3(static_cast<unsigned>((n + kThreads - 1) / kThreads)),
+                                   dim3(kThreads), 0, stream, a, n);
+  if (j != cudaSuccess) return j;
+  count_launches(1);
+  return cudaGetLastError();
 }
 
 }  // namespace
+
+// Two waves of CTAs (one to three fit on an SM, by d); 32 parts at most, so that
+// the partial sums stay within 64 times the bytes of k and v in fp32.
+int window_bwd_simt_parts(int64_t B, int64_t S, int Hkv, int G, int d) {
+  const int64_t tiles = (S + kT - 1) / kT, ctas = tiles * B * Hkv;
+  const int64_t want = 2 * static_cast<int64_t>(sm_count()) * (d == 128 ? 1 : (d == 64 ? 2 : 3));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want / ctas, tiles * G, 32})));
+}
 
 template <typename T>
 cudaError_t launch_window_simt(const WindowArgs& a, cudaStream_t stream) {

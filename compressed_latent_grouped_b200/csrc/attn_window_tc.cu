@@ -312,8 +312,13 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, FwdCfg<D>::kCtas)
     if (ok && mbar_wait(&o_done[x * 2 + ((n - 1) & 1)], ((n - 1) >> 1) & 1, &abort_flag, a.dev_err)) {
       tc_fence_after();
       const float inv_l = 1.f / l;
-      if (a.stats != nullptr && row_ok) a.stats[a.stat_row(bg, t, hl)] = -(m_used + log2f(l));
+      if (a.stats != nullptr && row_ok) {
+        const int64_t at = a.stat_row(bg, t, hl);
+        a.stats[at] = a.inv_l ? -m_used : -(m_used + log2f(l));
+        if (a.inv_l) a.inv_l[at] = inv_l;
+      }
       bf16* dst = static_cast<bf16*>(a.out.ptr) + b * a.out.batch + t * a.out.token + (g * G + hl) * a.out.head;
+      bf16* lo = a.o_lo + ((static_cast<int64_t>(b) * a.S + t) * a.Hq + g * G + hl) * D;
       uint8_t* stage = smem + C::kOffQ + x * C::kTileBytes + q4 * 2048;   // this tile's queries have been read
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -321,6 +326,15 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, FwdCfg<D>::kCtas)
         tmem_ld32(trow + C::col_o(x) + c * 32, o);
         tmem_wait_ld();
         warp_store32(row_ok ? dst + c * 32 : nullptr, o, inv_l, stage, lane);
+        if (a.o_lo != nullptr) {
+          // what the rounding dropped: the backward pass's D is that of the sum
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float x = __uint_as_float(o[e]) * inv_l;
+            o[e] = __float_as_uint(x - __bfloat162float(__float2bfloat16_rn(x)));
+          }
+          warp_store32(row_ok ? lo + c * 32 : nullptr, o, 1.f, stage, lane);
+        }
       }
     }
   }

@@ -300,16 +300,22 @@ struct WindowArgs {
   int B, S, Hq, Hkv, d, G;
   int window, sinks;            // at most S; window = S: the whole prefix
   Rows q, k, v, out;
-  // -log2(sum_s 2^(log2(e) q.k_s / sqrt(d))) and -rowsum(dO o) per query row,
-  // in groups of 64: pos = 64 / G positions with their G heads (G <= 64), else
-  // (pos = 0) t G + head; ld rows per (sequence, kv head)
+  // Per query row, in groups of 64 (pos = 64 / G positions with their G heads,
+  // G <= 64; else, pos = 0, row t G + head), ld rows per (sequence, kv head):
+  // with x_s = log2(e) q.k_s / sqrt(d), stats = -log2(sum_s 2^x_s) where the
+  // backward pass runs on the tensor core; elsewhere stats = -m and inv_l =
+  // 1 / sum_s 2^(x_s - m) with m = max x_s, two numbers because a probability
+  // formed from their one logarithm is off by its rounding.  dsum = -rowsum(dO o).
   float* stats;                 // forward: nullable
+  float* inv_l;                 // null on the tensor-core path
+  bf16* o_lo;                   // tensor-core path: what rounding took from out, [B, S, Hq, d]
   float* dsum;
   int64_t ld;
   int pos;
   // backward
   Rows dout, dq, dk, dv;
-  float* part;                  // tensor-core path: partial dk, dv sums
+  float* part;                  // partial dk, dv sums
+  int parts;                    // CUDA cores: CTAs that share a key tile
   int32_t* dev_err;
   __device__ __forceinline__ int64_t stat_row(int bg, int t, int hl) const {
     return bg * ld + (pos ? static_cast<int64_t>(t / pos) * 64 + t % pos * G : static_cast<int64_t>(t) * G) + hl;
@@ -321,8 +327,10 @@ cudaError_t launch_window_bwd_tc(const WindowArgs& a, cudaStream_t stream);
 size_t window_bwd_tc_part_floats(int d);   // of WindowArgs::part
 template <typename T>
 cudaError_t launch_window_simt(const WindowArgs& a, cudaStream_t stream);
+// parts: window_bwd_simt_parts; part (parts > 1): that many [B, S, Hkv, 2, d].
 template <typename T>
 cudaError_t launch_window_bwd_simt(const WindowArgs& a, cudaStream_t stream);
+int window_bwd_simt_parts(int64_t B, int64_t S, int Hkv, int G, int d);
 
 // Split plan for the decode step, shared by the workspace-size query and the launch.
 void decode_plan(int B, int Hkv, int E, int N, int64_t cap, bool has_proj, int es,
