@@ -61,7 +61,7 @@ class ccgqa_cache8(ctypes.Structure):
 class ccgqa_append(ctypes.Structure):
     _fields_ = [("q", ccgqa_rows), ("q_out", ccgqa_rows), ("k", ccgqa_rows), ("v", ccgqa_rows),
                 ("k_out", ccgqa_rows), ("n_new", c_int32), ("n_valid", c_void_p),
-                ("pos", c_void_p)]
+                ("pos", c_void_p), ("tickets", c_void_p)]
 
 
 class ccgqa_window(ctypes.Structure):
@@ -119,27 +119,28 @@ def load() -> ctypes.CDLL:
                                            c_int32, c_void_p, c_void_p, P(ccgqa_weight_grads),
                                            c_void_p, c_size_t, c_void_p, c_void_p]
     lib.ccgqa_prefill_backward.restype = c_int
-    lib.ccgqa_kvcache_append_rope.argtypes = [P(ccgqa_config), P(ccgqa_kvcache), P(ccgqa_cache8),
-                                              P(ccgqa_append), c_void_p, c_void_p]
+    # the small structures of these calls are also passed as packed bytes
+    R = c_void_p
+    lib.ccgqa_kvcache_append_rope.argtypes = [P(ccgqa_config), P(ccgqa_kvcache), P(ccgqa_cache8), R,
+                                              c_void_p, c_void_p]
     lib.ccgqa_kvcache_append_rope.restype = c_int
     lib.ccgqa_kvcache_read.argtypes = [P(ccgqa_config), P(ccgqa_kvcache), P(ccgqa_cache8), c_int32,
-                                       c_int32, P(ccgqa_rows), P(ccgqa_rows), c_void_p, c_void_p]
+                                       c_int32, R, R, c_void_p, c_void_p]
     lib.ccgqa_kvcache_read.restype = c_int
     lib.ccgqa_cache_attention_workspace_size.argtypes = [P(ccgqa_config), c_int32, c_int32]
     lib.ccgqa_cache_attention_workspace_size.restype = c_size_t
-    lib.ccgqa_cache_attention.argtypes = [P(ccgqa_config), P(ccgqa_window), P(ccgqa_kvcache),
+    lib.ccgqa_cache_attention.argtypes = [P(ccgqa_config), R, P(ccgqa_kvcache),
                                           P(ccgqa_cache8), c_void_p, c_void_p, c_void_p, c_size_t,
                                           c_void_p, c_void_p]
     lib.ccgqa_cache_attention.restype = c_int
-    R = P(ccgqa_rows)
     lib.ccgqa_window_attention_stats_size.argtypes = [P(ccgqa_config), c_int32, c_int32]
     lib.ccgqa_window_attention_stats_size.restype = c_size_t
-    lib.ccgqa_window_attention.argtypes = [P(ccgqa_config), P(ccgqa_window), R, R, R, c_int32, c_int32,
+    lib.ccgqa_window_attention.argtypes = [P(ccgqa_config), R, R, R, R, c_int32, c_int32,
                                            R, c_void_p, c_void_p, c_void_p]
     lib.ccgqa_window_attention.restype = c_int
     lib.ccgqa_window_attention_backward_workspace_size.argtypes = [P(ccgqa_config), c_int32, c_int32]
     lib.ccgqa_window_attention_backward_workspace_size.restype = c_size_t
-    lib.ccgqa_window_attention_backward.argtypes = [P(ccgqa_config), P(ccgqa_window), R, R, R, R, c_void_p,
+    lib.ccgqa_window_attention_backward.argtypes = [P(ccgqa_config), R, R, R, R, R, c_void_p,
                                                     R, c_int32, c_int32, R, R, R, c_void_p, c_size_t,
                                                     c_void_p, c_void_p]
     lib.ccgqa_window_attention_backward.restype = c_int
@@ -319,14 +320,11 @@ def ccgqa_prefill_backward(cfg, weights, x, batch, seq_len, dout, dx, grads, wor
     return st
 
 
-_NO_ROWS = ccgqa_rows(None, 0, 0, 0)
-
-
 def make_rows(t, order="bthd") -> ccgqa_rows:
     """Head rows of a 4-D tensor whose dimensions are batch, token, head and
     channel ("bthd") or batch, head, token and channel ("bhtd"); None: absent."""
     if t is None:
-        return _NO_ROWS
+        return ccgqa_rows(None, 0, 0, 0)
     b, x, y, _ = t.stride()
     return ccgqa_rows(t.data_ptr(), b, x, y) if order == "bthd" else ccgqa_rows(t.data_ptr(), b, y, x)
 

@@ -79,6 +79,7 @@ cudaError_t run_append(const Geo& g, const ccgqa_kvcache* c, const ccgqa_cache8*
   x.k_out = rows(a->k_out, g.Hkv);
   x.n_valid = a->n_valid;
   x.pos = a->pos;
+  x.tickets = a->tickets;
   x.rope_on = g.rope_on;
   if (g.rope_on) {
     // the fractions of the last (base, d): 64 powers in extended precision take
@@ -196,7 +197,7 @@ CCGQA_API ccgqa_status ccgqa_kvcache_append_rope(const ccgqa_config* cfg,
   if (a->q.ptr && (!rows_ok(g, a->q, B, n, g.Hq) || !rows_ok(g, a->q_out, B, n, g.Hq)))
     return CCGQA_ERR_INVALID_ARG;
   if (a->k_out.ptr && !rows_ok(g, a->k_out, B, n, g.Hkv)) return CCGQA_ERR_INVALID_ARG;
-  if (!aligned4(a->n_valid) || !aligned4(a->pos)) return CCGQA_ERR_INVALID_ARG;
+  if (!aligned4(a->n_valid) || !aligned4(a->pos) || !aligned4(a->tickets)) return CCGQA_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!stream_allowed(st)) return CCGQA_ERR_INVALID_ARG;
   const cudaError_t e = g.dtype == CCGQA_BF16 ? run_append<bf16>(g, cache, c8, a, dev_err, st)

@@ -244,8 +244,8 @@ struct AppendArgs {
   int rope_on;
   uint64_t rope_frac[64];       // as in PreAttnArgs
   int32_t* dev_err;
-  // set by the launcher
-  int tile_tokens, bump_here;
+  int32_t* tickets;             // nullable, [B]
+  int tile_tokens;              // set by the launcher
 };
 template <typename T>
 cudaError_t launch_append_rope(const AppendArgs<T>& a, int fmt, cudaStream_t stream);

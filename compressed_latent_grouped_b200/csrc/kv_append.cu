@@ -76,10 +76,8 @@ __device__ __forceinline__ float2 turn(int64_t pos, uint64_t frac) {
 // Rows of tokens [i0, i0 + tt): q (rotated) and, for a cache in the working
 // type, k (rotated) and v.
 template <typename T, bool kKv>
-__device__ __forceinline__ void append_rows(const AppendArgs<T>& a, int b, int i0, float2* cs) {
+__device__ __forceinline__ void append_rows(const AppendArgs<T>& a, int b, int L, int nv, int i0, float2* cs) {
   constexpr int V = Vec16<T>::N;
-  int L, nv;
-  if (!seq_span(a, b, i0 == 0 && threadIdx.x == 0, &L, &nv)) return;
   const int half = a.d >> 1, nch = half / V;
   const int tt = min(a.tile_tokens, nv - i0);
   const int64_t p0 = (a.pos ? a.pos[b] : L) + static_cast<int64_t>(i0);
@@ -129,12 +127,10 @@ __device__ __forceinline__ void append_rows(const AppendArgs<T>& a, int b, int i
 
 // One 8-bit block (token block j of kv head g, k or v).
 template <typename T, int FMT>
-__device__ __forceinline__ void append_block(const AppendArgs<T>& a, int b, int jj, int g, bool is_k,
+__device__ __forceinline__ void append_block(const AppendArgs<T>& a, int b, int L, int nv, int jj, int g, bool is_k,
                                              float* stash) {
   constexpr int V = Vec16<T>::N;
   __shared__ float red[kAppThreads / 32];
-  int L, nv;
-  if (!seq_span(a, b, jj == 0 && g == 0 && is_k && threadIdx.x == 0, &L, &nv)) return;
   const int blk = 1 << a.block_shift;
   const int64_t t0 = (static_cast<int64_t>(L >> a.block_shift) + jj) << a.block_shift;
   const int r0 = max(static_cast<int>(L - t0), 0);                 // first new row of the block
@@ -220,30 +216,38 @@ __device__ __forceinline__ void append_block(const AppendArgs<T>& a, int b, int 
 }
 
 // CTAs [0, n_blocks): the 8-bit blocks; the rest: tiles of tokens for the rows
-// stored in the working type.
+// stored in the working type.  With tickets, the last CTA of a sequence to have
+// read its length moves it on; which one that is does not show in any result.
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kAppThreads)
-    append_kernel(const __grid_constant__ AppendArgs<T> a, int n_blocks, int per_seq, int tiles) {
+    append_kernel(const __grid_constant__ AppendArgs<T> a, int n_blocks, int per_seq, int tiles, int ctas_per_seq) {
   pdl_enter();
   extern __shared__ __align__(16) uint8_t smem[];
-  int x = blockIdx.x;
-  if (FMT != 0 && x < n_blocks) {
-    const bool is_k = (x & 1) == 0;
-    x >>= 1;
-    const int g = x % a.Hkv;
-    x /= a.Hkv;
-    if constexpr (FMT != 0)
-      append_block<T, FMT>(a, x / per_seq, x % per_seq, g, is_k, reinterpret_cast<float*>(smem));
-    return;
+  const int x = blockIdx.x;
+  const bool block = FMT != 0 && x < n_blocks;
+  const int in_seq = block ? per_seq * a.Hkv * 2 : tiles;   // CTAs of this kind per sequence
+  const int y = block ? x : x - n_blocks;
+  const int b = y / in_seq, i = y % in_seq;
+  int L, nv;
+  const bool ok = seq_span(a, b, i == 0 && (block || n_blocks == 0) && threadIdx.x == 0, &L, &nv);
+  if (a.tickets) {
+    __syncthreads();   // every thread of this CTA holds the length
+    if (threadIdx.x == 0) {
+      __threadfence();
+      if (atomicAdd(a.tickets + b, 1) == ctas_per_seq - 1) {
+        a.tickets[b] = 0;
+        if (ok) a.len[b] = L + nv;
+      }
+    }
   }
-  x -= n_blocks;
-  const int b = x / tiles;
-  append_rows<T, FMT == 0>(a, b, (x % tiles) * a.tile_tokens, reinterpret_cast<float2*>(smem));
-  if (a.bump_here) {   // one tile holds all of a sequence's rows and no other CTA reads its length
-    __syncthreads();
-    int L, nv;
-    if (threadIdx.x == 0 && seq_span(a, b, false, &L, &nv)) a.len[b] = L + nv;
+  if (!ok) return;
+  if constexpr (FMT != 0) {
+    if (block) {
+      append_block<T, FMT>(a, b, L, nv, i / 2 / a.Hkv, i / 2 % a.Hkv, (i & 1) == 0, reinterpret_cast<float*>(smem));
+      return;
+    }
   }
+  append_rows<T, FMT == 0>(a, b, L, nv, i * a.tile_tokens, reinterpret_cast<float2*>(smem));
 }
 
 template <typename T>
@@ -266,16 +270,16 @@ cudaError_t launch_append_fmt(AppendArgs<T> a, cudaStream_t stream) {
   const int per_seq = FMT == 0 ? 1 : (a.n_new + 2 * blk - 2) / blk;
   const int64_t n_blocks = FMT == 0 ? 0 : static_cast<int64_t>(a.B) * per_seq * a.Hkv * 2;
   if (n_rows + n_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  a.bump_here = FMT == 0 && tiles == 1;
+  const int ctas_per_seq = static_cast<int>((n_rows + n_blocks) / a.B);
   size_t smem = static_cast<size_t>(a.tile_tokens) * half * sizeof(float2);
   if (FMT != 0 && static_cast<size_t>(blk) * a.d * 4 > smem) smem = static_cast<size_t>(blk) * a.d * 4;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(append_kernel<T, FMT>), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   e = launch_pdl(append_kernel<T, FMT>, dim3(static_cast<unsigned>(n_rows + n_blocks)), dim3(kAppThreads),
-                 smem, stream, a, static_cast<int>(n_blocks), per_seq, tiles);
+                 smem, stream, a, static_cast<int>(n_blocks), per_seq, tiles, ctas_per_seq);
   if (e != cudaSuccess) return e;
   count_launches(1);
-  if (!a.bump_here) {
+  if (!a.tickets) {
     e = launch_pdl(bump_kernel<T>, dim3((a.B + 127) / 128), dim3(128), 0, stream, a);
     if (e != cudaSuccess) return e;
     count_launches(1);

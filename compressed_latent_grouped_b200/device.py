@@ -3,6 +3,9 @@ cache, decode state, workspaces, the device error word) and this module hands
 pointers to the library.  No arithmetic of the method happens here."""
 from __future__ import annotations
 
+import ctypes
+import struct
+
 import torch
 
 from . import binding as B
@@ -176,31 +179,53 @@ def _check_dense(where, name, t, shape, dtype, device, optional=False):
 
 
 class _Call:
-    """The device and stream of one call: ``with _Call(device, stream) as raw``
-    makes the device current and gives the raw stream (the device's current one
-    for None).  Allocations inside come from that stream's pool, so that they go
-    back to it in its order."""
-
-    __slots__ = ("device", "stream", "contexts")
+    """The device and stream of one call where they are not the current ones:
+    makes the device current, and allocations inside come from the stream's
+    pool, so that they go back to it in its order."""
 
     def __init__(self, device, stream):
-        self.device, self.stream, self.contexts = device, stream, ()
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.device.index:
-            self.contexts = (torch.cuda.device(self.device),)
-        s = self.stream
-        if s is not None:
-            if isinstance(s, int):
-                s = torch.cuda.ExternalStream(s, device=self.device)
-            self.contexts += (torch.cuda.stream(s),)
+        self.contexts = [torch.cuda.device(device)]
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self.contexts.append(torch.cuda.stream(stream))
         for c in self.contexts:
             c.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
-    def __exit__(self, *exc):
+    def end(self):
         for c in reversed(self.contexts):
-            c.__exit__(*exc)
+            c.__exit__(None, None, None)
+
+
+def _begin(device, stream):
+    """(raw stream of a call, what to end after it or None)."""
+    call = None
+    if stream is not None or torch.cuda.current_device() != device.index:
+        call = _Call(device, stream)
+    return torch._C._cuda_getCurrentRawStream(device.index), call
+
+
+# ccgqa_rows, ccgqa_window and ccgqa_append as packed bytes (a third of the time
+# that filling ctypes structures takes)
+_pack_rows = struct.Struct("=4q").pack
+_pack_window = struct.Struct("=2i").pack
+_pack_append = struct.Struct("=20qi4x3q").pack
+_ABSENT = (0, 0, 0, 0)
+
+
+def _row_fields(t):
+    st = t.stride()
+    return t.data_ptr(), st[0], st[1], st[2]
+
+
+def _rows(t):
+    st = t.stride()
+    return _pack_rows(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _done(status, where):
+    if status:
+        raise B.CCGQAError(status, where)
 
 
 def head_dim(cfg: B.ccgqa_config) -> int:
@@ -291,6 +316,13 @@ class DeviceKVCache:
         self.cache = B.make_kvcache(k, v, len_, block_table=block_table)
         self.dev_err = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._attn_ws = B.ccgqa_cache_attention_workspace_size(cfg, self.batch, self.cap)
+        self._tickets = torch.zeros(self.batch, dtype=torch.int32, device=self.device)
+        self._Hq, self._Hkv = cfg.n_q_heads, cfg.n_kv_heads
+        # what every call passes
+        self._lib = B.load()
+        self._cfg, self._cache = ctypes.byref(cfg), ctypes.byref(self.cache)
+        self._c8 = None if self.cache8 is None else ctypes.byref(self.cache8)
+        self._err = self.dev_err.data_ptr()
 
     def append_rope(self, k, v, q=None, q_out=None, k_out=None, n_valid=None, pos=None, stream=None):
         """Append rows k, v [batch, n, Hkv, d], keys rotated; with q [batch, n,
@@ -301,44 +333,58 @@ class DeviceKVCache:
         if k.dim() != 4:
             _bad(where, "k is not 4-dimensional")
         n = k.shape[1]
-        kv = (self.batch, n, self.cfg.n_kv_heads, d)
-        qs = (self.batch, n, self.cfg.n_q_heads, d)
+        kv = (self.batch, n, self._Hkv, d)
         _check(where, "k", k, kv, dt, dev)
         _check(where, "v", v, kv, dt, dev)
-        _check(where, "k_out", k_out, kv, dt, dev, True)
-        if q is None and q_out is not None:
+        if k_out is not None:
+            _check(where, "k_out", k_out, kv, dt, dev)
+        if n_valid is not None:
+            _check_dense(where, "n_valid", n_valid, (self.batch,), torch.int32, dev)
+        if pos is not None:
+            _check_dense(where, "pos", pos, (self.batch,), torch.int32, dev)
+        qs = (self.batch, n, self._Hq, d)
+        if q is not None:
+            _check(where, "q", q, qs, dt, dev)
+            if q_out is not None:
+                _check(where, "q_out", q_out, qs, dt, dev)
+        elif q_out is not None:
             _bad(where, "q_out without q")
-        _check(where, "q", q, qs, dt, dev, True)
-        _check_dense(where, "n_valid", n_valid, (self.batch,), torch.int32, dev, True)
-        _check_dense(where, "pos", pos, (self.batch,), torch.int32, dev, True)
-        with _Call(dev, stream) as raw:
-            if q is not None:
-                if q_out is None:
-                    q_out = torch.empty(qs, dtype=dt, device=dev)
-                else:
-                    _check(where, "q_out", q_out, qs, dt, dev)
-            rows = B.make_rows
-            a = B.ccgqa_append(rows(q), rows(q_out), rows(k), rows(v), rows(k_out), n,
-                               None if n_valid is None else n_valid.data_ptr(),
-                               None if pos is None else pos.data_ptr())
-            B.ccgqa_kvcache_append_rope(self.cfg, self.cache, self.cache8, a, self.dev_err, raw)
+        raw, call = _begin(dev, stream)
+        try:
+            if q is not None and q_out is None:
+                q_out = torch.empty(qs, dtype=dt, device=dev)
+            f = _row_fields
+            _done(self._lib.ccgqa_kvcache_append_rope(
+                self._cfg, self._cache, self._c8,
+                _pack_append(*(_ABSENT if q is None else f(q)), *(_ABSENT if q is None else f(q_out)), *f(k), *f(v),
+                             *(_ABSENT if k_out is None else f(k_out)), n, 0 if n_valid is None else n_valid.data_ptr(),
+                             0 if pos is None else pos.data_ptr(), self._tickets.data_ptr()),
+                self._err, raw), "ccgqa_kvcache_append_rope")
+        finally:
+            if call is not None:
+                call.end()
         return q_out
 
     def read(self, first: int, n: int, k_out=None, v_out=None, stream=None):
         """Tokens [first, first + n) of every sequence as values, (k, v)
         [batch, Hkv, n, d]; rows past a sequence's length keep what the output
         held (zeros when allocated here)."""
-        shape = (self.batch, self.cfg.n_kv_heads, n, self.d)
-        with _Call(self.device, stream) as raw:
-            if k_out is None:
-                k_out = torch.zeros(shape, dtype=self.dtype, device=self.device)
-            if v_out is None:
-                v_out = torch.zeros(shape, dtype=self.dtype, device=self.device)
+        shape = (self.batch, self._Hkv, n, self.d)
+        if k_out is not None:
             _check("read", "k_out", k_out, shape, self.dtype, self.device)
+        if v_out is not None:
             _check("read", "v_out", v_out, shape, self.dtype, self.device)
-            B.ccgqa_kvcache_read(self.cfg, self.cache, self.cache8, first, n,
-                                 B.make_rows(k_out, "bhtd"), B.make_rows(v_out, "bhtd"), self.dev_err,
-                                 raw)
+        raw, call = _begin(self.device, stream)
+        try:
+            k_out, v_out = (torch.zeros(shape, dtype=self.dtype, device=self.device) if x is None else x
+                            for x in (k_out, v_out))
+            _done(self._lib.ccgqa_kvcache_read(self._cfg, self._cache, self._c8, first, n,
+                                               *(_pack_rows(p, b, t, h) for p, b, h, t in
+                                                 (_row_fields(k_out), _row_fields(v_out))), self._err, raw),
+                  "ccgqa_kvcache_read")
+        finally:
+            if call is not None:
+                call.end()
         return k_out, v_out
 
     def attend(self, q, out=None, window: int = 0, sinks: int = 0, stream=None):
@@ -346,34 +392,58 @@ class DeviceKVCache:
         over the cached tokens (with ``window`` > 0 the last ``window`` and the
         first ``sinks`` of them): out [batch, Hq, d].  Each call takes its
         workspace from torch's allocator."""
-        shape = (self.batch, self.cfg.n_q_heads, self.d)
+        shape = (self.batch, self._Hq, self.d)
         _check_dense("attend", "q", q, shape, self.dtype, self.device)
-        with _Call(self.device, stream) as raw:
+        if out is not None:
+            _check_dense("attend", "out", out, shape, self.dtype, self.device)
+        raw, call = _begin(self.device, stream)
+        try:
             if out is None:
                 out = torch.empty(shape, dtype=self.dtype, device=self.device)
-            else:
-                _check_dense("attend", "out", out, shape, self.dtype, self.device)
-            ws = None if self._attn_ws == 0 else torch.empty(self._attn_ws, dtype=torch.uint8, device=self.device)
-            B.ccgqa_cache_attention(self.cfg, B.ccgqa_window(window, sinks), self.cache, self.cache8, q, out,
-                                    ws, self.dev_err, raw)
+            ws, n = 0, self._attn_ws
+            if n:
+                scratch = torch.empty(n, dtype=torch.uint8, device=self.device)
+                ws = scratch.data_ptr()
+            _done(self._lib.ccgqa_cache_attention(self._cfg, _pack_window(window, sinks), self._cache, self._c8,
+                                                  q.data_ptr(), out.data_ptr(), ws, n, self._err, raw),
+                  "ccgqa_cache_attention")
+        finally:
+            if call is not None:
+                call.end()
         return out
 
     def error_bits(self) -> int:
         return int(self.dev_err.item())
 
 
+_sizes: dict = {}
+
+
+def _window_sizes(cfg, batch, S, index):
+    """(floats of statistics, workspace bytes of the backward pass) of a shape on
+    a device."""
+    key = (bytes(cfg), batch, S, index)
+    got = _sizes.get(key)
+    if got is None:
+        if len(_sizes) >= 1024:
+            _sizes.clear()
+        got = _sizes[key] = (B.ccgqa_window_attention_stats_size(cfg, batch, S),
+                             B.ccgqa_window_attention_backward_workspace_size(cfg, batch, S))
+    return got
+
+
 def _window_inputs(where, cfg, q, k, v):
     if q.dim() != 4:
         _bad(where, "q is not 4-dimensional")
-    batch, S = q.shape[:2]
-    dt, d = _dtype_of(cfg), head_dim(cfg)
-    if q.device.type != "cuda":
+    batch, S, _, _ = q.shape
+    dt, d, dev = _dtype_of(cfg), head_dim(cfg), q.device
+    if dev.type != "cuda":
         raise RuntimeError("CCGQA needs a CUDA device")
     q_shape, kv_shape = (batch, S, cfg.n_q_heads, d), (batch, S, cfg.n_kv_heads, d)
-    _check(where, "q", q, q_shape, dt, q.device)
-    _check(where, "k", k, kv_shape, dt, q.device)
-    _check(where, "v", v, kv_shape, dt, q.device)
-    return batch, S, dt, q.device, q_shape, kv_shape
+    _check(where, "q", q, q_shape, dt, dev)
+    _check(where, "k", k, kv_shape, dt, dev)
+    _check(where, "v", v, kv_shape, dt, dev)
+    return batch, S, dt, dev, q_shape, kv_shape
 
 
 def window_attention(cfg, q, k, v, window: int = 0, sinks: int = 0, out=None, with_stats: bool = False,
@@ -384,17 +454,22 @@ def window_attention(cfg, q, k, v, window: int = 0, sinks: int = 0, out=None, wi
     out, or with ``with_stats`` (out, stats), which the backward pass takes."""
     where = "window_attention"
     batch, S, dt, dev, q_shape, _ = _window_inputs(where, cfg, q, k, v)
-    with _Call(dev, stream) as raw:
+    if out is not None:
+        _check(where, "out", out, q_shape, dt, dev)
+    raw, call = _begin(dev, stream)
+    try:
         if out is None:
             out = torch.empty(q_shape, dtype=dt, device=dev)
-        else:
-            _check(where, "out", out, q_shape, dt, dev)
         stats = None
         if with_stats:
-            stats = torch.empty(B.ccgqa_window_attention_stats_size(cfg, batch, S), dtype=torch.float32, device=dev)
-        rows = B.make_rows
-        B.ccgqa_window_attention(cfg, B.ccgqa_window(window, sinks), rows(q), rows(k), rows(v), batch, S, rows(out),
-                                 stats, dev_err, raw)
+            stats = torch.empty(_window_sizes(cfg, batch, S, dev.index)[0], dtype=torch.float32, device=dev)
+        _done(B.load().ccgqa_window_attention(
+            ctypes.byref(cfg), _pack_window(window, sinks), _rows(q), _rows(k), _rows(v), batch, S, _rows(out),
+            None if stats is None else stats.data_ptr(), None if dev_err is None else dev_err.data_ptr(), raw),
+            "ccgqa_window_attention")
+    finally:
+        if call is not None:
+            call.end()
     return (out, stats) if with_stats else out
 
 
@@ -406,19 +481,27 @@ def window_attention_backward(cfg, q, k, v, out, stats, dout, window: int = 0, s
     batch, S, dt, dev, q_shape, kv_shape = _window_inputs(where, cfg, q, k, v)
     _check(where, "out", out, q_shape, dt, dev)
     _check(where, "dout", dout, q_shape, dt, dev)
-    _check_dense(where, "stats", stats, (B.ccgqa_window_attention_stats_size(cfg, batch, S),), torch.float32, dev)
-    _check(where, "dq", dq, q_shape, dt, dev, True)
-    _check(where, "dk", dk, kv_shape, dt, dev, True)
-    _check(where, "dv", dv, kv_shape, dt, dev, True)
-    with _Call(dev, stream) as raw:
-        dq, dk, dv = (torch.empty(shape, dtype=dt, device=dev) if x is None else x
-                      for x, shape in ((dq, q_shape), (dk, kv_shape), (dv, kv_shape)))
-        n = B.ccgqa_window_attention_backward_workspace_size(cfg, batch, S)
-        ws = None if n == 0 else torch.empty(n, dtype=torch.uint8, device=dev)
-        rows = B.make_rows
-        B.ccgqa_window_attention_backward(cfg, B.ccgqa_window(window, sinks), rows(q), rows(k), rows(v), rows(out),
-                                          stats, rows(dout), batch, S, rows(dq), rows(dk), rows(dv), ws, dev_err,
-                                          raw)
+    for name, x, shape in (("dq", dq, q_shape), ("dk", dk, kv_shape), ("dv", dv, kv_shape)):
+        if x is not None:
+            _check(where, name, x, shape, dt, dev)
+    raw, call = _begin(dev, stream)
+    try:
+        n_stats, n = _window_sizes(cfg, batch, S, dev.index)
+        _check_dense(where, "stats", stats, (n_stats,), torch.float32, dev)
+        if dq is None:
+            dq = torch.empty(q_shape, dtype=dt, device=dev)
+        if dk is None:
+            dk = torch.empty(kv_shape, dtype=dt, device=dev)
+        if dv is None:
+            dv = torch.empty(kv_shape, dtype=dt, device=dev)
+        scratch = torch.empty(n, dtype=torch.uint8, device=dev)
+        _done(B.load().ccgqa_window_attention_backward(
+            ctypes.byref(cfg), _pack_window(window, sinks), _rows(q), _rows(k), _rows(v), _rows(out), stats.data_ptr(),
+            _rows(dout), batch, S, _rows(dq), _rows(dk), _rows(dv), scratch.data_ptr(), n,
+            None if dev_err is None else dev_err.data_ptr(), raw), "ccgqa_window_attention_backward")
+    finally:
+        if call is not None:
+            call.end()
     return dq, dk, dv
 
 

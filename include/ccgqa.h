@@ -376,6 +376,9 @@ typedef struct {
   int32_t n_new;
   const int32_t* n_valid;
   const int32_t* pos;
+  int32_t* tickets;   /* nullable, [batch], zero before the first call, zero after each:
+                         with it the append is one launch (its last CTA that has
+                         read a length moves it on), without it two */
 } ccgqa_append;
 CCGQA_API ccgqa_status ccgqa_kvcache_append_rope(const ccgqa_config* cfg,
                                                  const ccgqa_kvcache* cache,

@@ -268,3 +268,26 @@ def test_streams_graphs_and_empty_calls():
     torch.cuda.synchronize()
     assert torch.equal(a.k, b.k) and torch.equal(a.v_scale, b.v_scale) and torch.equal(a.len, b.len)
     gr.close()
+
+
+@pytest.mark.parametrize("fmt", ["native", "i8"])
+def test_with_and_without_tickets(fmt):
+    """The length moves on by the append's last CTA or by a launch of its own."""
+    cfg = config(8, 2, 64, "bf16", 1e4)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    k = torch.randn(3, 70, 2, 64, generator=g, device="cuda").bfloat16()
+    q = torch.randn(3, 70, 8, 64, generator=g, device="cuda").bfloat16()
+    nv = torch.tensor([70, 0, 33], dtype=torch.int32).cuda()
+    a, b = (DeviceKVCache(cfg, 3, 256, fmt=fmt, block=32) for _ in range(2))
+    for n in (1, 70, 70):
+        qa = a.append_rope(k[:, :n], k[:, :n], q=q[:, :n], n_valid=nv.clamp(max=n))
+        qb = torch.empty_like(qa)
+        rows = B.make_rows
+        counts = nv.clamp(max=n)
+        B.ccgqa_kvcache_append_rope(cfg, b.cache, b.cache8, B.ccgqa_append(
+            rows(q[:, :n]), rows(qb), rows(k[:, :n]), rows(k[:, :n]), rows(None), n, counts.data_ptr(), None, None),
+            b.dev_err)
+        torch.cuda.synchronize()
+        assert torch.equal(a.len, b.len) and torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
+        assert torch.equal(qa[0], qb[0]) and not a._tickets.any()
+    assert a.len.tolist() == [141, 0, 67] and a.error_bits() == b.error_bits() == 0
