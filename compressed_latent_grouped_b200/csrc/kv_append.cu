@@ -11,20 +11,22 @@
 // element a sine per head would cost more than the memory traffic.
 //
 // 8-bit blocks: value = code * scale, scale = max(held scale, amax of the new
-// rows / qmax).  One CTA owns one block of one kv head, k or v: it keeps the
-// block's rotated rows as fp32 in shared memory, reduces their amax, rounds
-// again the codes that earlier calls stored if the scale grew, and writes the
-// new codes.  Nothing else writes that block, so no atomics are needed and the
+// rows / qmax).  The threads of one block of one kv head, k or v, keep its rotated
+// rows as fp32 in shared memory, reduce their amax, round again the codes that
+// earlier calls stored if the scale grew, and write the new codes; a CTA holds as
+// many such units of one token block as its threads have work for.  Nothing else writes that block, so no atomics are needed and the
 // result does not depend on the schedule.
 //
 // Bound: memory.  Every row is read once and written once.
+#include <algorithm>
+
 #include "cache_codes.cuh"
 
 namespace ccgqa {
 namespace {
 
 constexpr int kAppThreads = 256;
-constexpr float kTurn = 5.42101086242752217e-20f;   // 2^-64
+constexpr float kHalfTurns = 4.65661287307739258e-10f;   // 2^-31
 
 template <typename T>
 struct Vec16 {
@@ -41,9 +43,13 @@ __device__ __forceinline__ void load_vec(const T* p, float (&x)[16 / sizeof(T)])
 template <typename T>
 __device__ __forceinline__ void store_vec(T* p, const float (&x)[16 / sizeof(T)]) {
   uint4 r;
-  T* t = reinterpret_cast<T*>(&r);
+  if constexpr (sizeof(T) == 2) {
+    __nv_bfloat162* t = reinterpret_cast<__nv_bfloat162*>(&r);
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(16 / sizeof(T)); ++i) t[i] = from_f32<T>(x[i]);
+    for (int i = 0; i < 4; ++i) t[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+  } else {
+    r = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
   *reinterpret_cast<uint4*>(p) = r;
 }
 
@@ -67,18 +73,18 @@ __device__ __forceinline__ bool seq_span(const AppendArgs<T>& a, int b, bool rep
 }
 
 __device__ __forceinline__ float2 turn(int64_t pos, uint64_t frac) {
-  const uint64_t ph = static_cast<uint64_t>(pos) * frac;
+  // the top 32 bits of the fraction: 2^-33 turns are far below fp32's step of the angle
+  const int32_t ph = static_cast<int32_t>((static_cast<uint64_t>(pos) * frac) >> 32);
   float s, c;
-  sincospif(2.0f * (static_cast<float>(static_cast<int64_t>(ph)) * kTurn), &s, &c);
+  sincospif(static_cast<float>(ph) * kHalfTurns, &s, &c);
   return make_float2(c, s);
 }
 
 // Rows of tokens [i0, i0 + tt): q (rotated) and, for a cache in the working
 // type, k (rotated) and v.
-template <typename T, bool kKv>
+template <typename T, bool kKv, int D>
 __device__ __forceinline__ void append_rows(const AppendArgs<T>& a, int b, int L, int nv, int i0, float2* cs) {
-  constexpr int V = Vec16<T>::N;
-  const int half = a.d >> 1, nch = half / V;
+  constexpr int V = Vec16<T>::N, half = D / 2, nch = half / V;
   const int tt = min(a.tile_tokens, nv - i0);
   const int64_t p0 = (a.pos ? a.pos[b] : L) + static_cast<int64_t>(i0);
   if (a.rope_on)
@@ -87,8 +93,16 @@ __device__ __forceinline__ void append_rows(const AppendArgs<T>& a, int b, int L
   __syncthreads();
   const int n_q = a.q.ptr ? a.Hq : 0;
   const int heads = n_q + (kKv ? 2 * a.Hkv : 0);
-  for (int x = threadIdx.x; x < tt * heads * nch; x += kAppThreads) {
-    const int c = x % nch, hh = (x / nch) % heads, i = x / (nch * heads);
+  // thread: channels c of (row i, head hh), then step / heads rows and
+  // step % heads heads on (the chunks of half a head are a power of two)
+  const int c = threadIdx.x % nch, step = kAppThreads / nch;
+  const int row_step = step / heads, head_step = step % heads;
+  int i = threadIdx.x / nch / heads, hh = threadIdx.x / nch % heads;
+  for (; i < tt; i += row_step, hh += head_step) {
+    if (hh >= heads) {
+      hh -= heads;
+      if (++i >= tt) break;
+    }
     const bool is_q = hh < n_q, is_k = !is_q && hh < n_q + a.Hkv;
     const int h = is_q ? hh : (is_k ? hh - n_q : hh - n_q - a.Hkv);
     const Rows& src = is_q ? a.q : (is_k ? a.k : a.v);
@@ -117,7 +131,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs<T>& a, int b, int L
       if (row < 0) {
         raise_dev_err(a.dev_err, CCGQA_DEVERR_INDEX);
       } else {
-        T* o = static_cast<T*>(is_k ? a.ck : a.cv) + row * a.d + c * V;
+        T* o = static_cast<T*>(is_k ? a.ck : a.cv) + row * D + c * V;
         store_vec(o, lo);
         store_vec(o + half, hi);
       }
@@ -125,79 +139,95 @@ __device__ __forceinline__ void append_rows(const AppendArgs<T>& a, int b, int L
   }
 }
 
-// One 8-bit block (token block j of kv head g, k or v).
-template <typename T, int FMT>
-__device__ __forceinline__ void append_block(const AppendArgs<T>& a, int b, int L, int nv, int jj, int g, bool is_k,
-                                             float* stash) {
-  constexpr int V = Vec16<T>::N;
-  __shared__ float red[kAppThreads / 32];
+// 8-bit blocks: token block jj (counted from the one that holds token L) of the
+// units [u0, u0 + n): unit u < Hkv is kv head u's k, the others v.  `lanes` threads
+// work a unit, all of the same token block, so the CTA's control flow is uniform
+// and its rotation table serves every head.
+template <typename T, int FMT, int D>
+__device__ __forceinline__ void append_blocks(const AppendArgs<T>& a, int b, int L, int nv, int jj, int u0, int n,
+                                              int lanes, float* sm) {
+  constexpr int V = Vec16<T>::N, d = D, half = D / 2, nch = half / V, n8 = D / 8;
   const int blk = 1 << a.block_shift;
   const int64_t t0 = (static_cast<int64_t>(L >> a.block_shift) + jj) << a.block_shift;
   const int r0 = max(static_cast<int>(L - t0), 0);                 // first new row of the block
   const int64_t end = static_cast<int64_t>(L) + nv - t0;
   const int r1 = end < blk ? static_cast<int>(end) : blk;          // past its last new row
   if (r1 <= r0) return;
-  const int d = a.d, half = d >> 1, nch = half / V;
-  const Rows& src = is_k ? a.k : a.v;
-  const T* base = static_cast<const T*>(src.ptr) + b * src.batch + g * src.head;
   const int64_t i0 = t0 - L;                                       // new row index of block row 0
   const int64_t p0 = (a.pos ? a.pos[b] : L) + i0;
-  const bool rot = is_k && a.rope_on;
+  const int unit = threadIdx.x / lanes, lane = threadIdx.x & (lanes - 1);
+  const int u = u0 + unit;
+  const bool mine = unit < n;
+  const bool is_k = u < a.Hkv;
+  const int g = is_k ? u : u - a.Hkv;
+  // shared memory: rows as fp32 per unit, the rotation of (row, pair), a maximum per warp
+  float* stash = sm + unit * blk * d;
+  float2* cs = reinterpret_cast<float2*>(sm + (kAppThreads / lanes) * blk * d);
+  float* red = reinterpret_cast<float*>(cs + (a.rope_on ? blk * half : 0));
+  const bool table = a.rope_on && u0 < a.Hkv;
+  if (table) {
+    for (int x = threadIdx.x; x < (r1 - r0) * half; x += kAppThreads)
+      cs[x] = turn(p0 + r0 + x / half, a.rope_frac[x % half]);
+    __syncthreads();
+  }
   float amax = 0.f;
-  for (int x = threadIdx.x; x < (r1 - r0) * nch; x += kAppThreads) {
-    const int c = x % nch, r = r0 + x / nch;
-    const T* p = base + (i0 + r) * src.token + c * V;
-    float lo[V], hi[V];
-    load_vec(p, lo);
-    load_vec(p + half, hi);
-    if (rot) {
+  if (mine) {
+    const Rows& src = is_k ? a.k : a.v;
+    const T* base = static_cast<const T*>(src.ptr) + b * src.batch + g * src.head;
+    for (int x = lane; x < (r1 - r0) * nch; x += lanes) {
+      const int c = x % nch, r = r0 + x / nch;
+      const T* p = base + (i0 + r) * src.token + c * V;
+      float lo[V], hi[V];
+      load_vec(p, lo);
+      load_vec(p + half, hi);
+      if (is_k && a.rope_on) {
+        const float2* t = cs + (r - r0) * half + c * V;
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float2 t = turn(p0 + r, a.rope_frac[c * V + e]);
-        const float x0 = lo[e], x1 = hi[e];
-        lo[e] = x0 * t.x - x1 * t.y;
-        hi[e] = x0 * t.y + x1 * t.x;
+        for (int e = 0; e < V; ++e) {
+          const float x0 = lo[e], x1 = hi[e];
+          lo[e] = x0 * t[e].x - x1 * t[e].y;
+          hi[e] = x0 * t[e].y + x1 * t[e].x;
+        }
       }
-    }
-    float* s = stash + r * d + c * V;
+      float* s = stash + r * d + c * V;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      amax = max_nan(amax, max_nan(fabsf(lo[e]), fabsf(hi[e])));
-      s[e] = lo[e];
-      s[half + e] = hi[e];
-    }
-    if (is_k && a.k_out.ptr) {
-      T* o = static_cast<T*>(a.k_out.ptr) + b * a.k_out.batch + (i0 + r) * a.k_out.token +
-             g * a.k_out.head + c * V;
-      store_vec(o, lo);
-      store_vec(o + half, hi);
+      for (int e = 0; e < V; e += 4) {
+        *reinterpret_cast<float4*>(s + e) = make_float4(lo[e], lo[e + 1], lo[e + 2], lo[e + 3]);
+        *reinterpret_cast<float4*>(s + half + e) = make_float4(hi[e], hi[e + 1], hi[e + 2], hi[e + 3]);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) amax = max_nan(amax, max_nan(fabsf(lo[e]), fabsf(hi[e])));
+      if (is_k && a.k_out.ptr) {
+        T* o = static_cast<T*>(a.k_out.ptr) + b * a.k_out.batch + (i0 + r) * a.k_out.token +
+               g * a.k_out.head + c * V;
+        store_vec(o, lo);
+        store_vec(o + half, hi);
+      }
     }
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-  __syncthreads();
-  amax = red[0];
-#pragma unroll
-  for (int w = 1; w < kAppThreads / 32; ++w) amax = max_nan(amax, red[w]);
-  const int64_t row0 = kv_row(a.pages, b, g, a.Hkv, a.cap, t0);
+  // held scale of the block; rows are in whole blocks everywhere, so its index is row / block
+  const int64_t row0 = mine ? kv_row(a.pages, b, g, a.Hkv, a.cap, t0) : -2;
+  float* scale = (is_k ? a.k_scale : a.v_scale) + (row0 >= 0 ? row0 >> a.block_shift : 0);
+  const float s_old = row0 >= 0 && r0 > 0 ? *scale : 0.f;
+  __syncthreads();   // also: every thread has read the held scale
+  if (!mine) return;
   if (row0 < 0) {
-    if (threadIdx.x == 0) raise_dev_err(a.dev_err, CCGQA_DEVERR_INDEX);
+    if (lane == 0) raise_dev_err(a.dev_err, CCGQA_DEVERR_INDEX);
     return;
   }
-  // rows are in whole blocks everywhere, so a block's scale index is its row / block
-  float* scale = (is_k ? a.k_scale : a.v_scale) + (row0 >> a.block_shift);
+  amax = 0.f;
+  for (int w = 0; w < lanes / 32; ++w) amax = max_nan(amax, red[unit * (lanes / 32) + w]);
   constexpr float kMaxCode = FMT == kCacheI8 ? 127.0f : 448.0f;
-  const float s_old = r0 > 0 ? *scale : 0.f;
   const float s_new = max_nan(s_old, amax / kMaxCode);
   const float by = s_new == 0.f ? 1.0f : s_new;   // a block of zeros keeps scale 0
-  __syncthreads();   // every thread has read the held scale
-  if (threadIdx.x == 0) *scale = s_new;
+  if (lane == 0) *scale = s_new;
   uint8_t* codes = static_cast<uint8_t*>(is_k ? a.ck : a.cv) + row0 * d;
-  const int n8 = d >> 3;
   if (s_new > s_old && r0 > 0) {
     const float ratio = s_old / s_new;
-    for (int x = threadIdx.x; x < r0 * n8; x += kAppThreads) {
+    for (int x = lane; x < r0 * n8; x += lanes) {
       uint2* w = reinterpret_cast<uint2*>(codes + x * 8);
       float v[8];
       decode8<FMT>(*w, v);
@@ -206,11 +236,20 @@ __device__ __forceinline__ void append_block(const AppendArgs<T>& a, int b, int 
       *w = encode8<FMT>(v);
     }
   }
-  for (int x = threadIdx.x; x < (r1 - r0) * n8; x += kAppThreads) {
-    const float* s = stash + r0 * d + x * 8;
-    float v[8];
+  // x / scale as x (1 / scale) with one residual correction (Markstein's), which
+  // leaves the quotient correctly rounded but for the rarest cases; divided where
+  // 1 / scale or the residual leaves the normal range
+  const float inv = 1.0f / by;
+  const bool plain = by > 1e-30f && by < 1e30f;
+  for (int x = lane; x < (r1 - r0) * n8; x += lanes) {
+    const float4* s = reinterpret_cast<const float4*>(stash + r0 * d + x * 8);
+    const float4 f0 = s[0], f1 = s[1];
+    float v[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = s[e] / by;
+    for (int e = 0; e < 8; ++e) {
+      const float q = v[e] * inv;
+      v[e] = plain ? fmaf(fmaf(-q, by, v[e]), inv, q) : v[e] / by;
+    }
     *reinterpret_cast<uint2*>(codes + r0 * d + x * 8) = encode8<FMT>(v);
   }
 }
@@ -218,14 +257,17 @@ __device__ __forceinline__ void append_block(const AppendArgs<T>& a, int b, int 
 // CTAs [0, n_blocks): the 8-bit blocks; the rest: tiles of tokens for the rows
 // stored in the working type.  With tickets, the last CTA of a sequence to have
 // read its length moves it on; which one that is does not show in any result.
-template <typename T, int FMT>
+template <typename T, int FMT, int D>
 __global__ void __launch_bounds__(kAppThreads)
-    append_kernel(const __grid_constant__ AppendArgs<T> a, int n_blocks, int per_seq, int tiles, int ctas_per_seq) {
+    append_kernel(const __grid_constant__ AppendArgs<T> a, int n_blocks, int per_seq, int tiles, int ctas_per_seq,
+                  int lanes_shift) {
   pdl_enter();
   extern __shared__ __align__(16) uint8_t smem[];
   const int x = blockIdx.x;
   const bool block = FMT != 0 && x < n_blocks;
-  const int in_seq = block ? per_seq * a.Hkv * 2 : tiles;   // CTAs of this kind per sequence
+  const int lanes = 1 << lanes_shift, units = kAppThreads >> lanes_shift;
+  const int groups = (2 * a.Hkv + units - 1) / units;
+  const int in_seq = block ? per_seq * groups : tiles;      // CTAs of this kind per sequence
   const int y = block ? x : x - n_blocks;
   const int b = y / in_seq, i = y % in_seq;
   int L, nv;
@@ -243,11 +285,12 @@ __global__ void __launch_bounds__(kAppThreads)
   if (!ok) return;
   if constexpr (FMT != 0) {
     if (block) {
-      append_block<T, FMT>(a, b, L, nv, i / 2 / a.Hkv, i / 2 % a.Hkv, (i & 1) == 0, reinterpret_cast<float*>(smem));
+      const int u0 = i % groups * units;
+      append_blocks<T, FMT, D>(a, b, L, nv, i / groups, u0, min(units, 2 * a.Hkv - u0), lanes, reinterpret_cast<float*>(smem));
       return;
     }
   }
-  append_rows<T, FMT == 0>(a, b, L, nv, i * a.tile_tokens, reinterpret_cast<float2*>(smem));
+  append_rows<T, FMT == 0, D>(a, b, L, nv, i * a.tile_tokens, reinterpret_cast<float2*>(smem));
 }
 
 template <typename T>
@@ -258,25 +301,36 @@ __global__ void __launch_bounds__(128) bump_kernel(const __grid_constant__ Appen
   if (b < a.B && seq_span(a, b, false, &L, &nv)) a.len[b] = L + nv;
 }
 
-template <typename T, int FMT>
-cudaError_t launch_append_fmt(AppendArgs<T> a, cudaStream_t stream) {
-  const int half = a.d / 2;
-  a.tile_tokens = kAppThreads / half > 0 ? kAppThreads / half : 1;
-  const int tiles = (a.n_new + a.tile_tokens - 1) / a.tile_tokens;
+template <typename T, int FMT, int D>
+cudaError_t launch_append_d(AppendArgs<T> a, cudaStream_t stream) {
+  constexpr int half = D / 2, nch = half / Vec16<T>::N;
   const bool rows = FMT == 0 || a.q.ptr;
+  // tiles of tokens: two rounds of a CTA's threads over their heads
+  const int per_token = ((a.q.ptr ? a.Hq : 0) + (FMT == 0 ? 2 * a.Hkv : 0)) * nch;
+  a.tile_tokens = rows ? std::min(std::max(2 * kAppThreads / per_token, 1), 1024 / half) : 1;
+  const int tiles = (a.n_new + a.tile_tokens - 1) / a.tile_tokens;
   const int64_t n_rows = rows ? static_cast<int64_t>(a.B) * tiles : 0;
   const int blk = 1 << a.block_shift;
   // a run of n_new tokens that starts anywhere in a block touches this many blocks
   const int per_seq = FMT == 0 ? 1 : (a.n_new + 2 * blk - 2) / blk;
-  const int64_t n_blocks = FMT == 0 ? 0 : static_cast<int64_t>(a.B) * per_seq * a.Hkv * 2;
+  // threads per (head, k or v): a warp per 1024 elements, so that a thread has two
+  // pairs of 16-byte loads at bf16
+  int lanes_shift = 5;
+  while (lanes_shift < 8 && (32 << lanes_shift) < blk * D) ++lanes_shift;
+  const int units = kAppThreads >> lanes_shift, groups = (2 * a.Hkv + units - 1) / units;
+  const int64_t n_blocks = FMT == 0 ? 0 : static_cast<int64_t>(a.B) * per_seq * groups;
   if (n_rows + n_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const int ctas_per_seq = static_cast<int>((n_rows + n_blocks) / a.B);
   size_t smem = static_cast<size_t>(a.tile_tokens) * half * sizeof(float2);
-  if (FMT != 0 && static_cast<size_t>(blk) * a.d * 4 > smem) smem = static_cast<size_t>(blk) * a.d * 4;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(append_kernel<T, FMT>), static_cast<int>(smem));
+  if (FMT != 0) {
+    const size_t need = sizeof(float) * (static_cast<size_t>(units) * blk * D + (a.rope_on ? static_cast<size_t>(blk) * D : 0) +
+                                         kAppThreads / 32);
+    if (need > smem) smem = need;
+  }
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(append_kernel<T, FMT, D>), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  e = launch_pdl(append_kernel<T, FMT>, dim3(static_cast<unsigned>(n_rows + n_blocks)), dim3(kAppThreads),
-                 smem, stream, a, static_cast<int>(n_blocks), per_seq, tiles, ctas_per_seq);
+  e = launch_pdl(append_kernel<T, FMT, D>, dim3(static_cast<unsigned>(n_rows + n_blocks)), dim3(kAppThreads), smem,
+                 stream, a, static_cast<int>(n_blocks), per_seq, tiles, ctas_per_seq, lanes_shift);
   if (e != cudaSuccess) return e;
   count_launches(1);
   if (!a.tickets) {
@@ -287,51 +341,70 @@ cudaError_t launch_append_fmt(AppendArgs<T> a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <typename T, int FMT>
+cudaError_t launch_append_fmt(const AppendArgs<T>& a, cudaStream_t stream) {
+  switch (a.d) {
+    case 16: return launch_append_d<T, FMT, 16>(a, stream);
+    case 32: return launch_append_d<T, FMT, 32>(a, stream);
+    case 64: return launch_append_d<T, FMT, 64>(a, stream);
+    case 128: return launch_append_d<T, FMT, 128>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 // ----------------------------------------------------------------- read back
+// CTA: 256 pieces of 8 channels of one (sequence, kv head), k and v.
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kAppThreads)
-    kv_read_kernel(const __grid_constant__ ReadArgs a, int64_t total) {
+    kv_read_kernel(const __grid_constant__ ReadArgs a, int per_head, int nch_shift) {
   pdl_enter();
-  constexpr int V = 8;
-  const int nch = a.d / V;
-  for (int64_t x = static_cast<int64_t>(blockIdx.x) * kAppThreads + threadIdx.x; x < total;
-       x += static_cast<int64_t>(gridDim.x) * kAppThreads) {
-    const int c = static_cast<int>(x % nch);
-    int64_t y = x / nch;
-    const int i = static_cast<int>(y % a.n);   // tokens of a head are neighbours in the cache
-    y /= a.n;
-    const int g = static_cast<int>(y % a.Hkv), b = static_cast<int>(y / a.Hkv);
-    const int L = a.len[b];
-    if (L < 0 || L > a.cap) {
-      if (i == 0 && g == 0 && c == 0) raise_dev_err(a.dev_err, CCGQA_DEVERR_CAPACITY);
-      continue;
+  const int bg = blockIdx.x / per_head, g = bg % a.Hkv, b = bg / a.Hkv;
+  const int x = (blockIdx.x - bg * per_head) * kAppThreads + threadIdx.x;
+  const int i = x >> nch_shift, c = (x & ((1 << nch_shift) - 1)) * 8;
+  const int L = a.len[b];
+  if (L < 0 || L > a.cap) {
+    if (x == 0 && g == 0) raise_dev_err(a.dev_err, CCGQA_DEVERR_CAPACITY);
+    return;
+  }
+  const int64_t t = static_cast<int64_t>(a.first) + i;
+  if (i >= a.n || t >= L) return;
+  const int64_t row = kv_row(a.pages, b, g, a.Hkv, a.cap, t);
+  if (row < 0) {
+    raise_dev_err(a.dev_err, CCGQA_DEVERR_INDEX);
+    return;
+  }
+  constexpr int W = sizeof(T) / 2;   // 16-byte stores of a piece
+  uint4 raw[2][W];
+  uint2 code[2];
+  float scale[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    if constexpr (FMT == 0) {
+      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const T*>(w ? a.cv : a.ck) + row * a.d + c);
+#pragma unroll
+      for (int u = 0; u < W; ++u) raw[w][u] = s[u];
+    } else {
+      code[w] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(w ? a.cv : a.ck) + row * a.d + c);
+      scale[w] = (w ? a.v_scale : a.k_scale)[row >> a.block_shift];
     }
-    const int64_t t = static_cast<int64_t>(a.first) + i;
-    if (t >= L) continue;
-    const int64_t row = kv_row(a.pages, b, g, a.Hkv, a.cap, t);
-    if (row < 0) {
-      raise_dev_err(a.dev_err, CCGQA_DEVERR_INDEX);
-      continue;
-    }
+  }
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const Rows& dst = w ? a.v_out : a.k_out;
-      T* o = static_cast<T*>(dst.ptr) + b * dst.batch + i * dst.token + g * dst.head + c * V;
-      if constexpr (FMT == 0) {
-        const uint4* s = reinterpret_cast<const uint4*>(static_cast<const T*>(w ? a.cv : a.ck) + row * a.d + c * V);
+  for (int w = 0; w < 2; ++w) {
+    const Rows& dst = w ? a.v_out : a.k_out;
+    T* o = static_cast<T*>(dst.ptr) + b * dst.batch + i * dst.token + g * dst.head + c;
+    if constexpr (FMT == 0) {
 #pragma unroll
-        for (int u = 0; u < static_cast<int>(V * sizeof(T) / 16); ++u) reinterpret_cast<uint4*>(o)[u] = s[u];
-      } else {
-        float v[8];
-        decode8<FMT>(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(w ? a.cv : a.ck) + row * a.d + c * V), v);
-        const float s = (w ? a.v_scale : a.k_scale)[row >> a.block_shift];
-        float f[16 / sizeof(T)];
+      for (int u = 0; u < W; ++u) reinterpret_cast<uint4*>(o)[u] = raw[w][u];
+    } else {
+      float v[8];
+      decode8<FMT>(code[w], v);
+      constexpr int N = 16 / sizeof(T);
+      float f[N];
 #pragma unroll
-        for (int u = 0; u < static_cast<int>(V * sizeof(T) / 16); ++u) {
+      for (int u = 0; u < W; ++u) {
 #pragma unroll
-          for (int e = 0; e < static_cast<int>(16 / sizeof(T)); ++e) f[e] = v[u * (16 / sizeof(T)) + e] * s;
-          store_vec(o + u * (16 / sizeof(T)), f);
-        }
+        for (int e = 0; e < N; ++e) f[e] = v[u * N + e] * scale[w];
+        store_vec(o + u * N, f);
       }
     }
   }
@@ -339,11 +412,13 @@ __global__ void __launch_bounds__(kAppThreads)
 
 template <typename T, int FMT>
 cudaError_t launch_read_fmt(const ReadArgs& a, cudaStream_t stream) {
-  const int64_t total = static_cast<int64_t>(a.B) * a.Hkv * a.n * (a.d / 8);
-  const int64_t want = (total + kAppThreads - 1) / kAppThreads;
-  const int64_t most = static_cast<int64_t>(sm_count()) * 64;
-  const cudaError_t e = launch_pdl(kv_read_kernel<T, FMT>, dim3(static_cast<unsigned>(want < most ? want : most)),
-                                   dim3(kAppThreads), 0, stream, a, total);
+  int shift = 0;
+  while ((8 << shift) < a.d) ++shift;   // d / 8 pieces of a row
+  const int64_t per_head = ((static_cast<int64_t>(a.n) << shift) + kAppThreads - 1) / kAppThreads;
+  const int64_t grid = per_head * a.B * a.Hkv;
+  if (grid > 0x7fffffff || (static_cast<int64_t>(a.n) << shift) > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = launch_pdl(kv_read_kernel<T, FMT>, dim3(static_cast<unsigned>(grid)), dim3(kAppThreads), 0,
+                                   stream, a, static_cast<int>(per_head), shift);
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();
