@@ -7,7 +7,7 @@
 // Query rows are packed per kv group as in the causal kernel: row r of a tile is
 // position t0 + r / G, head g G + r % G, gathered by a 5-D TMA box from any
 // strides; a tile holds floor(128 / G) positions, rows past them are zeroed
-// once.  One CTA owns T consecutive query tiles of one kv group and walks the
+// once.  One CTA owns T (one to three) consecutive query tiles of one kv group and walks the
 // key pieces (64 keys) they see: the sinks' pieces, then the window's, whose first
 // key is the first one any of its rows sees: a TMA box may start at any row, so
 // a window of W keys costs W + (positions of the CTA) keys rounded up to 64, not
@@ -40,7 +40,7 @@ constexpr int kPiece = 64;
 // Every probability stays below this (times 64 keys): see exp_pass.
 constexpr float kSumLimit = 1024.0f;
 
-template <int D>
+template <int D, int T>
 struct FwdCfg : RowTiles<D> {
   using R = RowTiles<D>;
   static constexpr uint32_t kTileBytes = 128 * D * 2;         // one Q tile
@@ -48,8 +48,8 @@ struct FwdCfg : RowTiles<D> {
   static constexpr uint32_t kPanelQ = 128 * R::kRowBytes;
   static constexpr uint32_t kPanelK = kPiece * R::kRowBytes;
   static constexpr int kStages = D == 128 ? 4 : (D == 64 ? 5 : 8);
-  static constexpr int kTiles = D == 64 ? 1 : (D == 32 ? 3 : 2);
-  static constexpr int kCtas = D == 64 ? 2 : 1;               // on an SM
+  static constexpr int kTiles = T;
+  static constexpr int kCtas = T == 1 && D <= 64 ? 2 : 1;     // on an SM
   // one pair in kSoftEvery takes the FMA pipe's exponential (the best shares of
   // the causal kernel, whose softmax this is)
   static constexpr int kSoftEvery = D == 64 ? 3 : (D == 32 ? 5 : 4);
@@ -66,13 +66,13 @@ struct FwdCfg : RowTiles<D> {
   __device__ static constexpr uint32_t col_o(int x) { return kTiles * 128 + x * D; }
 };
 
-template <int D>
-__global__ void __launch_bounds__(FwdCfg<D>::kThreads, FwdCfg<D>::kCtas)
+template <int D, int T>
+__global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, FwdCfg<D, T>::kCtas)
     window_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WindowArgs a,
                          int n_groups) {
   pdl_enter();
-  using C = FwdCfg<D>;
+  using C = FwdCfg<D, T>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -348,9 +348,9 @@ __global__ void __launch_bounds__(FwdCfg<D>::kThreads, FwdCfg<D>::kCtas)
   }
 }
 
-template <int D>
+template <int D, int T>
 cudaError_t launch_fwd(const WindowArgs& a, cudaStream_t stream) {
-  using C = FwdCfg<D>;
+  using C = FwdCfg<D, T>;
   CUtensorMap tmQ, tmK, tmV;
   if (!packed_rows_map(&tmQ, a.q, a, 128 / a.G) || !key_rows_map(&tmK, a.k, a, kPiece) ||
       !key_rows_map(&tmV, a.v, a, kPiece))
@@ -359,9 +359,9 @@ cudaError_t launch_fwd(const WindowArgs& a, cudaStream_t stream) {
   const int64_t n_groups = (a.S + per_cta - 1) / per_cta;
   const int64_t grid = n_groups * a.B * a.Hkv;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_fwd_tc_kernel<D>), static_cast<int>(C::kSmem));
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_fwd_tc_kernel<D, T>), static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
-  e = launch_pdl(window_fwd_tc_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), C::kSmem, stream, tmQ,
+  e = launch_pdl(window_fwd_tc_kernel<D, T>, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), C::kSmem, stream, tmQ,
                  tmK, tmV, a, static_cast<int>(n_groups));
   if (e != cudaSuccess) return e;
   count_launches(1);
@@ -372,10 +372,17 @@ cudaError_t launch_fwd(const WindowArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_window_tc(const WindowArgs& a, cudaStream_t stream) {
   if (a.G > 128) return cudaErrorInvalidValue;
+  // Tiles per CTA.  d = 64: one, two CTAs on an SM, whose starts and ends hide
+  // behind each other (S = 16384, window 1024: 76 us; two tiles in one CTA: 83).
+  // d = 32: three share the key pieces (4 x 4096, window 1024: 94 us; one: 102),
+  // d = 128: two; but one while the tiles fit on the GPU at once (2 x 301 positions
+  // at d = 32: 6.1 us against 9.6).
+  const int64_t pos = 128 / a.G, tiles = (a.S + pos - 1) / pos * a.B * a.Hkv;
+  const bool few = tiles <= static_cast<int64_t>(sm_count()) * (a.d == 32 ? 2 : 1);
   switch (a.d) {
-    case 32: return launch_fwd<32>(a, stream);
-    case 64: return launch_fwd<64>(a, stream);
-    case 128: return launch_fwd<128>(a, stream);
+    case 32: return few ? launch_fwd<32, 1>(a, stream) : launch_fwd<32, 3>(a, stream);
+    case 64: return launch_fwd<64, 1>(a, stream);
+    case 128: return few ? launch_fwd<128, 1>(a, stream) : launch_fwd<128, 2>(a, stream);
     default: return cudaErrorInvalidValue;
   }
 }
