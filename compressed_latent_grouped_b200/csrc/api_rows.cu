@@ -164,10 +164,12 @@ size_t window_dsum_bytes(const Geo& g, int64_t B, int64_t S) {
   return up256(static_cast<size_t>(B * g.Hkv * stat_rows(g, S)) * sizeof(float));
 }
 size_t window_bwd_workspace(const Geo& g, int64_t B, int64_t S) {
-  size_t part = window_bwd_tc_part_floats(g.d);
-  if (!window_tc(g, 64)) {
+  size_t part = 0;
+  if (window_tc(g, 64)) {
+    part = window_bwd_tc_part_floats(B, S, g.Hkv, g.G, g.d);
+  } else {
     const int parts = window_bwd_simt_parts(B, S, g.Hkv, g.G, g.d);
-    part = parts > 1 ? static_cast<size_t>(parts) * B * S * g.Hkv * 2 * g.d : 0;
+    if (parts > 1) part = static_cast<size_t>(parts) * B * S * g.Hkv * 2 * g.d;
   }
   return window_dsum_bytes(g, B, S) + part * sizeof(float);
 }

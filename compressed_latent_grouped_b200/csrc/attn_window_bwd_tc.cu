@@ -782,30 +782,39 @@ __global__ void __launch_bounds__(256)
 
 // Share the blocks out evenly; a share holds at least kMinBlocks.
 constexpr int64_t kMinBlocks = 2;
+int64_t blocks_of(const WindowArgs& a, int pos, int tile) {
+  const int2 g = dkv_groups(tile, a.S, a.window, a.sinks, pos);
+  return (g.y - g.x) / 2 + 1;
+}
+int cta_count(int64_t blocks) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sm_count(), kMaxCtas, blocks / kMinBlocks})));
+}
 void make_plan(const WindowArgs& a, DkvPlan* p) {
   p->pos = 64 / a.G;
   p->n_tiles = (a.S + kRows - 1) / kRows;
   const int64_t BH = static_cast<int64_t>(a.B) * a.Hkv;
-  auto blocks = [&](int tile) {
-    const int2 g = dkv_groups(tile, a.S, a.window, a.sinks, p->pos);
-    return static_cast<int64_t>((g.y - g.x) / 2 + 1);
-  };
+  // blocks before every step-th tile of a (sequence, kv head)
+  constexpr int kMarks = 256;
+  int64_t mark[kMarks + 1];
+  const int step = (p->n_tiles + kMarks - 1) / kMarks;
   int64_t per = 0;
-  for (int i = 0; i < p->n_tiles; ++i) per += blocks(i);
+  int marks = 0;
+  for (int i = 0; i < p->n_tiles; ++i) {
+    if (i % step == 0) mark[marks++] = per;
+    per += blocks_of(a, p->pos, i);
+  }
   const int64_t total = per * BH;
-  p->n_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sm_count(), kMaxCtas, total / kMinBlocks})));
-  int64_t at = 0;       // blocks of (sequence, kv head) bg before tile x
-  int64_t bg = 0;
-  int x = 0;
+  p->n_ctas = cta_count(total);
   for (int c = 0; c <= p->n_ctas; ++c) {
     const int64_t u = total / p->n_ctas * c + std::min<int64_t>(total % p->n_ctas, c);
-    if (u / per != bg) {
-      bg = u / per;
-      at = 0;
-      x = 0;
+    const int64_t bg = u / per, rem = u - bg * per;
+    const int m = static_cast<int>(std::upper_bound(mark, mark + marks, rem) - mark) - 1;
+    int x = m * step;
+    int64_t at = mark[m];
+    for (int64_t n = blocks_of(a, p->pos, x); at + n <= rem; n = blocks_of(a, p->pos, x)) {
+      at += n;
+      ++x;
     }
-    const int64_t rem = u - bg * per;
-    while (x < p->n_tiles && at + blocks(x) <= rem) at += blocks(x++);
     p->start[c] = make_int2(static_cast<int>(bg * p->n_tiles + x), static_cast<int>(rem - at));
   }
   // a CTA that starts inside a tile continues the one before it
@@ -853,7 +862,12 @@ cudaError_t launch_bwd(const WindowArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t window_bwd_tc_part_floats(int d) { return static_cast<size_t>(kMaxCtas) * 2 * kRows * 2 * d; }
+// Two tiles per CTA of the plan for the whole prefix, which has the most blocks.
+size_t window_bwd_tc_part_floats(int64_t B, int64_t S, int Hkv, int G, int d) {
+  const int64_t tiles = (S + kRows - 1) / kRows, groups = (S + 64 / G - 1) / (64 / G);
+  const int64_t most = tiles * (groups / 2 + 1) * B * Hkv;
+  return static_cast<size_t>(cta_count(most)) * 2 * kRows * 2 * d;
+}
 
 cudaError_t launch_window_bwd_tc(const WindowArgs& a, cudaStream_t stream) {
   if (a.G > 64) return cudaErrorInvalidValue;

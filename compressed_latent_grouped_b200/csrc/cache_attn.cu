@@ -86,7 +86,7 @@ struct Visible {
 
 // Length of sequence b; zero, and an error bit, when it is outside [0, cap].
 __device__ __forceinline__ int checked_len(const CacheAttnArgs& a, int b, bool report) {
-  const int L = __ldg(a.len + b);
+  const int L = __ldcg(a.len + b);
   if (L >= 0 && L <= a.cap) return L;
   if (report) raise_dev_err(a.dev_err, CCGQA_DEVERR_CAPACITY);
   return 0;
@@ -650,13 +650,13 @@ __global__ void __launch_bounds__(kCaThreads)
   const float cs = kLog2eC * rsqrtf(static_cast<float>(D));
   auto fetch = [&](const void* base, int64_t row, float (&x)[4]) {
     if constexpr (FMT == 0) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + row * D + e0));
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + row * D + e0));
       x[0] = v.x;
       x[1] = v.y;
       x[2] = v.z;
       x[3] = v.w;
     } else {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(base) + row * D + e0));
+      const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(base) + row * D + e0));
       float y[8];
       decode8<FMT>(make_uint2(w, 0), y);
 #pragma unroll
@@ -670,8 +670,8 @@ __global__ void __launch_bounds__(kCaThreads)
       if (lane == 0) raise_dev_err(a.dev_err, CCGQA_DEVERR_INDEX);
       continue;
     }
-    const float sk = FMT == 0 ? cs : cs * __ldg(a.k_scale + (rb >> a.block_shift));
-    const float sv = FMT == 0 ? 1.f : __ldg(a.v_scale + (rb >> a.block_shift));
+    const float sk = FMT == 0 ? cs : cs * __ldcg(a.k_scale + (rb >> a.block_shift));
+    const float sv = FMT == 0 ? 1.f : __ldcg(a.v_scale + (rb >> a.block_shift));
 #pragma unroll
     for (int u0 = 0; u0 < kSteps; u0 += U) {
       float k[U][4], v[U][4];
@@ -841,9 +841,8 @@ cudaError_t launch_fmt(const CacheAttnArgs& a, int fmt, cudaStream_t stream) {
 
 }  // namespace
 
-// Splits that fill two waves of CTAs and spill into no third (64 sequences of
-// 16384 int8 tokens, 2 kv heads of 64: 61.5 us with 10 splits, 2.2 waves, XX us
-// with 9), each of at least 512 tokens.
+// Splits that fill two waves of CTAs and spill into no third, each of at least
+// 512 tokens.
 int cache_attn_splits(int64_t units, int64_t keys, int ctas_per_sm) {
   const int64_t want = static_cast<int64_t>(sm_count()) * ctas_per_sm * 2 / units;
   const int64_t most = (keys + 511) / 512;

@@ -324,7 +324,8 @@ struct WindowArgs {
 // bf16, d in {32, 64, 128}: tcgen05, for G <= 128 (forward) and G <= 64 (backward).
 cudaError_t launch_window_tc(const WindowArgs& a, cudaStream_t stream);
 cudaError_t launch_window_bwd_tc(const WindowArgs& a, cudaStream_t stream);
-size_t window_bwd_tc_part_floats(int d);   // of WindowArgs::part
+// Floats of WindowArgs::part for any window.
+size_t window_bwd_tc_part_floats(int64_t B, int64_t S, int Hkv, int G, int d);
 template <typename T>
 cudaError_t launch_window_simt(const WindowArgs& a, cudaStream_t stream);
 // parts: window_bwd_simt_parts; part (parts > 1): that many [B, S, Hkv, 2, d].

@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+import threading
 
 import torch
 
@@ -205,6 +206,25 @@ def _begin(device, stream):
     return torch._C._cuda_getCurrentRawStream(device.index), call
 
 
+_recording = threading.local()
+
+
+def _empty(shape, dtype, device):
+    """What a call allocates.  While a Graph records, it is kept with the graph,
+    whose replays use the memory."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    kept = getattr(_recording, "tensors", None)
+    if kept is not None:
+        kept.append(t)
+    return t
+
+
+def _window_of(where, window, sinks):
+    if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
+        _bad(where, f"window {window} and sinks {sinks} are not counts")
+    return _pack_window(window, sinks)
+
+
 # ccgqa_rows, ccgqa_window and ccgqa_append as packed bytes (a third of the time
 # that filling ctypes structures takes)
 _pack_rows = struct.Struct("=4q").pack
@@ -264,6 +284,8 @@ class DeviceKVCache:
         H, d = cfg.n_kv_heads, head_dim(cfg)
         lead, rows = ((batch, H), cap) if block_table is None else ((n_pages, H), page_size)
         dt = _dtype_of(cfg) if fmt == "native" else self.FORMATS[fmt][1]
+        if block_table is not None:
+            block_table = block_table.to(dev, torch.int32).contiguous()
         kv = [torch.zeros(*lead, rows, d, dtype=torch.uint8 if fmt == "e4m3" else dt, device=dev).view(dt)
               for _ in range(2)]
         sc = [None, None] if fmt == "native" else [
@@ -296,7 +318,7 @@ class DeviceKVCache:
         if block_table is not None:
             if block_table.dim() != 2:
                 _bad(where, "block_table is not 2-dimensional")
-            block_table = block_table.to(self.device, torch.int32).contiguous()
+            _check_dense(where, "block_table", block_table, tuple(block_table.shape), torch.int32, self.device)
         self.batch = k.shape[0] if block_table is None else block_table.shape[0]
         self.cap = k.shape[2] if block_table is None else block_table.shape[1] * k.shape[2]
         _check_dense(where, "len", len_, (self.batch,), torch.int32, self.device)
@@ -352,7 +374,7 @@ class DeviceKVCache:
         raw, call = _begin(dev, stream)
         try:
             if q is not None and q_out is None:
-                q_out = torch.empty(qs, dtype=dt, device=dev)
+                q_out = _empty(qs, dt, dev)
             f = _row_fields
             _done(self._lib.ccgqa_kvcache_append_rope(
                 self._cfg, self._cache, self._c8,
@@ -376,7 +398,7 @@ class DeviceKVCache:
             _check("read", "v_out", v_out, shape, self.dtype, self.device)
         raw, call = _begin(self.device, stream)
         try:
-            k_out, v_out = (torch.zeros(shape, dtype=self.dtype, device=self.device) if x is None else x
+            k_out, v_out = (_empty(shape, self.dtype, self.device).zero_() if x is None else x
                             for x in (k_out, v_out))
             _done(self._lib.ccgqa_kvcache_read(self._cfg, self._cache, self._c8, first, n,
                                                *(_pack_rows(p, b, t, h) for p, b, h, t in
@@ -392,19 +414,19 @@ class DeviceKVCache:
         over the cached tokens (with ``window`` > 0 the last ``window`` and the
         first ``sinks`` of them): out [batch, Hq, d].  Each call takes its
         workspace from torch's allocator."""
-        shape = (self.batch, self._Hq, self.d)
-        _check_dense("attend", "q", q, shape, self.dtype, self.device)
+        where, shape = "attend", (self.batch, self._Hq, self.d)
+        _check_dense(where, "q", q, shape, self.dtype, self.device)
         if out is not None:
-            _check_dense("attend", "out", out, shape, self.dtype, self.device)
+            _check_dense(where, "out", out, shape, self.dtype, self.device)
         raw, call = _begin(self.device, stream)
         try:
             if out is None:
-                out = torch.empty(shape, dtype=self.dtype, device=self.device)
+                out = _empty(shape, self.dtype, self.device)
             ws, n = 0, self._attn_ws
             if n:
-                scratch = torch.empty(n, dtype=torch.uint8, device=self.device)
+                scratch = _empty(n, torch.uint8, self.device)
                 ws = scratch.data_ptr()
-            _done(self._lib.ccgqa_cache_attention(self._cfg, _pack_window(window, sinks), self._cache, self._c8,
+            _done(self._lib.ccgqa_cache_attention(self._cfg, _window_of(where, window, sinks), self._cache, self._c8,
                                                   q.data_ptr(), out.data_ptr(), ws, n, self._err, raw),
                   "ccgqa_cache_attention")
         finally:
@@ -456,15 +478,17 @@ def window_attention(cfg, q, k, v, window: int = 0, sinks: int = 0, out=None, wi
     batch, S, dt, dev, q_shape, _ = _window_inputs(where, cfg, q, k, v)
     if out is not None:
         _check(where, "out", out, q_shape, dt, dev)
+    if dev_err is not None:
+        _check_dense(where, "dev_err", dev_err, (1,), torch.int32, dev)
     raw, call = _begin(dev, stream)
     try:
         if out is None:
-            out = torch.empty(q_shape, dtype=dt, device=dev)
+            out = _empty(q_shape, dt, dev)
         stats = None
         if with_stats:
-            stats = torch.empty(_window_sizes(cfg, batch, S, dev.index)[0], dtype=torch.float32, device=dev)
+            stats = _empty(_window_sizes(cfg, batch, S, dev.index)[0], torch.float32, dev)
         _done(B.load().ccgqa_window_attention(
-            ctypes.byref(cfg), _pack_window(window, sinks), _rows(q), _rows(k), _rows(v), batch, S, _rows(out),
+            ctypes.byref(cfg), _window_of(where, window, sinks), _rows(q), _rows(k), _rows(v), batch, S, _rows(out),
             None if stats is None else stats.data_ptr(), None if dev_err is None else dev_err.data_ptr(), raw),
             "ccgqa_window_attention")
     finally:
@@ -484,19 +508,21 @@ def window_attention_backward(cfg, q, k, v, out, stats, dout, window: int = 0, s
     for name, x, shape in (("dq", dq, q_shape), ("dk", dk, kv_shape), ("dv", dv, kv_shape)):
         if x is not None:
             _check(where, name, x, shape, dt, dev)
+    if dev_err is not None:
+        _check_dense(where, "dev_err", dev_err, (1,), torch.int32, dev)
     raw, call = _begin(dev, stream)
     try:
         n_stats, n = _window_sizes(cfg, batch, S, dev.index)
         _check_dense(where, "stats", stats, (n_stats,), torch.float32, dev)
         if dq is None:
-            dq = torch.empty(q_shape, dtype=dt, device=dev)
+            dq = _empty(q_shape, dt, dev)
         if dk is None:
-            dk = torch.empty(kv_shape, dtype=dt, device=dev)
+            dk = _empty(kv_shape, dt, dev)
         if dv is None:
-            dv = torch.empty(kv_shape, dtype=dt, device=dev)
-        scratch = torch.empty(n, dtype=torch.uint8, device=dev)
+            dv = _empty(kv_shape, dt, dev)
+        scratch = _empty(n, torch.uint8, dev)
         _done(B.load().ccgqa_window_attention_backward(
-            ctypes.byref(cfg), _pack_window(window, sinks), _rows(q), _rows(k), _rows(v), _rows(out), stats.data_ptr(),
+            ctypes.byref(cfg), _window_of(where, window, sinks), _rows(q), _rows(k), _rows(v), _rows(out), stats.data_ptr(),
             _rows(dout), batch, S, _rows(dq), _rows(dk), _rows(dv), scratch.data_ptr(), n,
             None if dev_err is None else dev_err.data_ptr(), raw), "ccgqa_window_attention_backward")
     finally:
@@ -515,6 +541,7 @@ class Graph:
         self.stream = stream
         self.handle = None
         B.ccgqa_graph_begin(stream)
+        _recording.tensors = self.tensors = []
         try:
             with torch.cuda.stream(stream):
                 fn()
@@ -524,6 +551,8 @@ class Graph:
             except B.CCGQAError:
                 pass
             raise
+        finally:
+            _recording.tensors = None
         self.handle = B.ccgqa_graph_end(stream)
         self.kernels = B.ccgqa_graph_kernel_count(self.handle)
 
@@ -534,3 +563,4 @@ class Graph:
         if self.handle is not None:
             B.ccgqa_graph_destroy(self.handle)
             self.handle = None
+            self.tensors = []

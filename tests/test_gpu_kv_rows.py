@@ -291,3 +291,46 @@ def test_with_and_without_tickets(fmt):
         assert torch.equal(a.len, b.len) and torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
         assert torch.equal(qa[0], qb[0]) and not a._tickets.any()
     assert a.len.tolist() == [141, 0, 67] and a.error_bits() == b.error_bits() == 0
+
+
+@pytest.mark.parametrize("fmt", ["native", "i8"])
+def test_positions_given_as_the_lengths(fmt):
+    """pos may be the cache's own len tensor, which the call moves on."""
+    cfg = config(16, 4, 64, "bf16", 1e4)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    k = torch.randn(2, 700, 4, 64, generator=g, device="cuda").bfloat16()
+    q = torch.randn(2, 700, 16, 64, generator=g, device="cuda").bfloat16()
+    a, b = (DeviceKVCache(cfg, 2, 2048, fmt=fmt, block=32) for _ in range(2))
+    for _ in range(2):
+        qa, qb = a.append_rope(k, k, q=q), b.append_rope(k, k, q=q, pos=b.len)
+        assert torch.equal(qa, qb) and torch.equal(a.k, b.k)
+    assert a.len.tolist() == b.len.tolist() == [1400, 1400]
+
+
+def test_python_refusals():
+    cfg = config(8, 2, 64)
+    c = DeviceKVCache(cfg, 2, 128)
+    k = torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(2, 8, 64, dtype=torch.bfloat16, device="cuda")
+    bad = [
+        lambda: c.append_rope(k[:, :, 0], k), lambda: c.append_rope(k, k[:, :2]), lambda: c.append_rope(k.float(), k),
+        lambda: c.append_rope(k.cpu(), k), lambda: c.append_rope(k, k.transpose(2, 3).contiguous().transpose(2, 3)),
+        lambda: c.append_rope(k, k, q_out=k), lambda: c.append_rope(k, k, n_valid=torch.zeros(2, device="cuda")),
+        lambda: c.append_rope(k, k, pos=torch.zeros(3, dtype=torch.int32, device="cuda")),
+        lambda: c.append_rope(k.expand(2, 3, 2, 64)[:1].expand(2, 3, 2, 64), k),      # one row for both sequences
+        lambda: c.read(0, 129), lambda: c.read(-1, 3), lambda: c.read(0, 3, k_out=k),
+        lambda: c.attend(q[:1]), lambda: c.attend(q.float()), lambda: c.attend(q, out=q[:, :4]),
+        lambda: c.attend(q, window=-1), lambda: c.attend(q, window=1 << 31), lambda: c.attend(q, sinks=-2),
+        lambda: DeviceKVCache(cfg, 2, 128, fmt="fp4"), lambda: DeviceKVCache(cfg, 2, 128, fmt="i8", block=48),
+        lambda: DeviceKVCache(cfg, 2, 96, fmt="i8", block=64),
+        lambda: DeviceKVCache.wrap(cfg, c.k, c.v, c.len, k_scale=torch.zeros(2, 2, 2, device="cuda")),
+        lambda: DeviceKVCache.wrap(cfg, c.k.to(torch.int8), c.v.to(torch.int8), c.len),
+        lambda: DeviceKVCache.wrap(cfg, c.k, c.v, c.len, block_table=torch.zeros(2, 1, dtype=torch.int64, device="cuda")),
+        lambda: DeviceKVCache.wrap(cfg, c.k, c.v[:, :1], c.len), lambda: DeviceKVCache.wrap(cfg, c.k, c.v, c.len[:1]),
+    ]
+    n = B.ccgqa_launch_count()
+    for i, f in enumerate(bad):
+        with pytest.raises(B.CCGQAError):
+            f()
+            pytest.fail(f"call {i} was accepted")
+    assert B.ccgqa_launch_count() == n and c.len.tolist() == [0, 0]

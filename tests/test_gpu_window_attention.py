@@ -248,3 +248,69 @@ def test_prompt_then_tokens():
     close(last, ref["out"][:, -1], tol["out"][:, -1], "token")
     assert c.error_bits() == 0
     assert np.array_equal(c.k[:, :, :300].float().cpu().numpy(), kr.transpose(1, 2).float().cpu().numpy())
+
+
+def test_recorded_calls_keep_their_memory():
+    """What calls allocate while the library's graph records stays with the graph."""
+    from compressed_latent_grouped_b200.device import DeviceKVCache
+    cfg = config(8, 2, 64)
+    q, k, v, do = inputs(1, 900, 8, 2, 64, "bf16", seed=8)
+    kw = dict(window=300, sinks=4)
+    c = DeviceKVCache(cfg, 1, 4096)
+    c.append_rope(k, v)
+    qt = q[:, -1].contiguous()
+    grads = [torch.empty_like(x) for x in (q, k, v)]
+    row = torch.empty_like(qt)
+    s = torch.cuda.Stream()
+
+    def step():
+        out, stats = window_attention(cfg, q, k, v, with_stats=True, **kw)
+        window_attention_backward(cfg, q, k, v, out, stats, do, dq=grads[0], dk=grads[1], dv=grads[2], **kw)
+        c.attend(qt, out=row)
+
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    ref = [x.clone() for x in (*grads, row)]
+    g = Graph(step, s)
+    with torch.cuda.stream(s):          # the stream's pool is drawn on by others meanwhile
+        others = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (1 << 12, 1 << 20, 1 << 22, 1 << 24)
+                  for _ in range(6)]
+    for _ in range(3):
+        for x in (*grads, row):
+            x.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.launch()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*grads, row), ref))
+        assert all(bool((o == 255).all()) for o in others)
+    g.close()
+
+
+def test_python_refusals():
+    cfg = config(8, 2, 64)
+    q, k, v, do = inputs(2, 40, 8, 2, 64, "bf16")
+    out, stats = window_attention(cfg, q, k, v, with_stats=True)
+    two_way = config(8, 2, 64)
+    two_way.causal = 0
+    bad = [
+        lambda: window_attention(cfg, q[0], k, v), lambda: window_attention(cfg, q, k[:, :39], v),
+        lambda: window_attention(cfg, q, k, v.float()), lambda: window_attention(cfg, q, k.cpu(), v),
+        lambda: window_attention(cfg, q, k, v, window=-3), lambda: window_attention(cfg, q, k, v, sinks=1 << 40),
+        lambda: window_attention(cfg, q, k, v, out=out[:1]), lambda: window_attention(two_way, q, k, v),
+        lambda: window_attention(cfg, q, k, v, dev_err=torch.zeros(1, device="cuda")),
+        lambda: window_attention(cfg, q, k[:, :1].expand(2, 40, 2, 64), v),       # keys that share memory
+        lambda: window_attention_backward(cfg, q, k, v, out, stats[:-1], do),
+        lambda: window_attention_backward(cfg, q, k, v, out, None, do),
+        lambda: window_attention_backward(cfg, q, k, v, out, stats, do[:, :, :4]),
+        lambda: window_attention_backward(cfg, q, k, v, out, stats, torch.ones(1, 1, 1, 1, dtype=q.dtype, device="cuda").expand_as(do)),
+        lambda: window_attention_backward(cfg, q, k, v, out, stats, do, dk=torch.empty_like(q)),
+    ]
+    n = B.ccgqa_launch_count()
+    for i, f in enumerate(bad):
+        with pytest.raises(B.CCGQAError):
+            f()
+            pytest.fail(f"call {i} was accepted")
+    assert B.ccgqa_launch_count() == n
+    with pytest.raises(RuntimeError):
+        window_attention(cfg, q.cpu(), k.cpu(), v.cpu())
