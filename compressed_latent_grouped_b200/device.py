@@ -219,6 +219,18 @@ def _empty(shape, dtype, device):
     return t
 
 
+def _like(t):
+    """A dense tensor of t's shape and type, as _empty (half its time where t is
+    dense itself)."""
+    if not t.is_contiguous():
+        return _empty(t.shape, t.dtype, t.device)
+    r = torch.empty_like(t)
+    kept = getattr(_recording, "tensors", None)
+    if kept is not None:
+        kept.append(r)
+    return r
+
+
 def _window_of(where, window, sinks):
     if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
         _bad(where, f"window {window} and sinks {sinks} are not counts")
@@ -374,7 +386,7 @@ class DeviceKVCache:
         raw, call = _begin(dev, stream)
         try:
             if q is not None and q_out is None:
-                q_out = _empty(qs, dt, dev)
+                q_out = _like(q)
             f = _row_fields
             _done(self._lib.ccgqa_kvcache_append_rope(
                 self._cfg, self._cache, self._c8,
@@ -421,7 +433,7 @@ class DeviceKVCache:
         raw, call = _begin(self.device, stream)
         try:
             if out is None:
-                out = _empty(shape, self.dtype, self.device)
+                out = _like(q)
             ws, n = 0, self._attn_ws
             if n:
                 scratch = _empty(n, torch.uint8, self.device)
@@ -483,7 +495,7 @@ def window_attention(cfg, q, k, v, window: int = 0, sinks: int = 0, out=None, wi
     raw, call = _begin(dev, stream)
     try:
         if out is None:
-            out = _empty(q_shape, dt, dev)
+            out = _like(q)
         stats = None
         if with_stats:
             stats = _empty(_window_sizes(cfg, batch, S, dev.index)[0], torch.float32, dev)
@@ -515,11 +527,11 @@ def window_attention_backward(cfg, q, k, v, out, stats, dout, window: int = 0, s
         n_stats, n = _window_sizes(cfg, batch, S, dev.index)
         _check_dense(where, "stats", stats, (n_stats,), torch.float32, dev)
         if dq is None:
-            dq = _empty(q_shape, dt, dev)
+            dq = _like(q)
         if dk is None:
-            dk = _empty(kv_shape, dt, dev)
+            dk = _like(k)
         if dv is None:
-            dv = _empty(kv_shape, dt, dev)
+            dv = _like(v)
         scratch = _empty(n, torch.uint8, dev)
         _done(B.load().ccgqa_window_attention_backward(
             ctypes.byref(cfg), _window_of(where, window, sinks), _rows(q), _rows(k), _rows(v), _rows(out), stats.data_ptr(),
