@@ -24,12 +24,22 @@
 //   O += P V    the scores leave S in the layout the next product wants P in.
 //               V's fragment pairs two tokens of one channel: a byte permute of
 //               the two tokens' words, then the conversion.
-// int8 codes become fp16 exactly by placing the byte (plus 128) in the mantissa
-// of 1024 and subtracting 1152; e4m3 codes by the hardware's conversion.  q is
-// scaled by a power of two per head into fp16's range (exact for all but
-// elements 2^-28 below the largest), the probabilities, times their block's v
-// scale, are rounded to fp16 after a second running max, of x + log2 sv, has
-// brought them near one.  Against a cache in bf16 both stay in bf16.
+// int8 keys are multiplied as they are: q becomes a 16-bit integer per head (off
+// by at most 2^-15 of the head's largest element), its high and low bytes two rows
+// of the s8 product, whose integer sums are exact (conversion of the keys to fp16
+// instead: 61 us against 54 below).  e4m3 keys become fp16 by the hardware's
+// conversion, q is scaled by a power of two per head into fp16's range (exact for
+// all but elements 2^-28 below the largest).  int8 values become fp16 exactly by
+// placing the byte (plus 128) in the mantissa of 1024 and subtracting 1152.  The
+// probabilities, times their block's v scale, are rounded to fp16 after a second
+// running max, of x + log2 sv, has brought them near one.  Against a cache in bf16
+// q and the probabilities stay in bf16.
+//
+// 64 sequences of 16384 tokens, 8 / 2 heads of 64, int8: 54 us, 5.0 TB/s; 16 ragged
+// ones of up to 8192, 32 / 8 heads of 128, e4m3: 48 us, 3.5 TB/s; a window of 4096
+// over bf16, 32 sequences: 16 us, 4.2 TB/s.  The bound is the conversions' and the
+// softmax's issue slots (16 warps an SM at 64 channels and 12 at 128 issue in half
+// of the cycles), not the memory.
 //
 // fp32 layers.  CUDA cores, fp32 throughout, chunks of four query heads: d / 4
 // lanes share a token, each with four channels.
@@ -57,6 +67,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float fmaxf_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan3(float a, float b, float c) { return fmaxf_nan(a, fmaxf_nan(b, c)); }
 __device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
 
 // ----------------------------------------------------------------- visible tokens
@@ -166,6 +182,19 @@ __device__ __forceinline__ void mma16(float* d, const uint32_t* a, uint32_t b0, 
 #undef CCGQA_MMA
 #undef CCGQA_COMMA
 
+// D (+)= A B, 16 x 32 by 32 x 8 signed bytes.
+template <bool kFirst>
+__device__ __forceinline__ void mma_s8(int32_t (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (kFirst)
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(0));
+  else
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 // Copy of 16 or 4 bytes to shared memory; zeros when !on.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
@@ -231,7 +260,7 @@ __global__ void __launch_bounds__(kCaThreads, (D == 128 && FMT == 0) || MR == 2 
     cache_attn_kernel(const CacheAttnArgs a) {
   pdl_enter();
   using C = CaCfg<D, FMT>;
-  constexpr bool kHalf = FMT != 0, kTop = MR == 1;
+  constexpr bool kHalf = FMT != 0, kTop = MR == 1, kBytes = FMT == kCacheI8;
   constexpr int NT = C::kTile / 8, KS = D / 16, NV = D / 8, kA = MR == 1 ? 2 : 4;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -329,14 +358,17 @@ __global__ void __launch_bounds__(kCaThreads, (D == 128 && FMT == 0) || MR == 2 
   }
 
   // ---- Q fragments: head r (and r + 8), channels in the order of K's pieces
-  uint32_t qf[KS][kA];
+  constexpr int kEl = C::kPieceK / C::kEs;      // channels of a piece
+  // int8: fragments of 32 channels, [0]: the high bytes of q (MR = 1: in rows 0..7,
+  // the low bytes in rows 8..15), [1] (MR = 2): the low bytes
+  constexpr int kWords = kBytes ? C::kPieceK / 4 : 0, KB = kBytes ? (D >= 32 ? D / 32 : 1) : 1;
+  uint32_t qf[KS][kA], qb[KB][MR][4];
   float cs[MR];   // score of an accumulator, in units of log2
 #pragma unroll
   for (int m = 0; m < MR; ++m) {
     const int h = r + 8 * m;
     const bf16* q = static_cast<const bf16*>(a.q) + (static_cast<int64_t>(b) * a.Hq + h0 + h) * D;
-    constexpr int kEl = C::kPieceK / C::kEs;   // channels of a piece
-    uint2 w[KS];
+    uint2 w[KS];   // four channels: of step k, or word k of the pieces
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       const int ch = (c + 4 * (k * 4 / kEl)) * kEl + k * 4 % kEl;
@@ -349,27 +381,56 @@ __global__ void __launch_bounds__(kCaThreads, (D == 128 && FMT == 0) || MR == 2 
       for (int k = 0; k < KS; ++k) {
         const float2 x = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[k].x));
         const float2 y = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[k].y));
-        top = fmaxf(top, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
+        top = max_nan3(top, fmaxf_nan(fabsf(x.x), fabsf(x.y)), fmaxf_nan(fabsf(y.x), fabsf(y.y)));
       }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // largest element to [2^14, 2^15); zero, tiny and infinite ones keep a finite scale
+      top = fmaxf_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // largest element to [2^14, 2^15); zero and tiny ones keep a finite scale, and
+      // a head with an infinity or NaN has only NaN scores
       int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xffu) - 127;
       e = min(max(e, -100), 126);
       const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
       cs[m] *= __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+      if (!(top < INFINITY)) cs[m] = __uint_as_float(0x7fc00000u);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const float2 x = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[k].x));
         const float2 y = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[k].y));
-        w[k] = make_uint2(pack16<true>(x.x * up, x.y * up), pack16<true>(y.x * up, y.y * up));
+        if constexpr (kBytes) {
+          // q 2^(14 - e) as a 16-bit integer 256 hi + lo (the largest mantissa one short)
+          const float v[4] = {x.x, x.y, y.x, y.y};
+          uint32_t hi = 0, lo = 0;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int f = __float2int_rn(fminf(fmaxf(v[u] * up, -32639.f), 32639.f));
+            const int f_hi = (f + 128) >> 8;
+            hi |= (static_cast<uint32_t>(f_hi) & 0xffu) << (8 * u);
+            lo |= (static_cast<uint32_t>(f - 256 * f_hi) & 0xffu) << (8 * u);
+          }
+          // word k: k-slots (k & 1) of fragment k / 2; a[0], a[1]: rows r, r + 8
+          if (MR == 1) {
+            qb[k / 2][0][(k & 1) * 2] = hi;
+            qb[k / 2][0][(k & 1) * 2 + 1] = lo;
+          } else {
+            qb[k / 2][0][(k & 1) * 2 + m] = hi;
+            qb[k / 2][MR - 1][(k & 1) * 2 + m] = lo;
+          }
+        } else {
+          w[k] = make_uint2(pack16<true>(x.x * up, x.y * up), pack16<true>(y.x * up, y.y * up));
+        }
+      }
+      if (kBytes && KS == 1) {   // d = 16: the fragment's upper 16 channels are zero
+#pragma unroll
+        for (int v = 0; v < MR; ++v) qb[0][v][2] = qb[0][v][3] = 0;
       }
     }
+    if constexpr (!kBytes) {
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      // A's registers: (row r, k lo), (row r + 8, k lo), (r, k hi), (r + 8, k hi)
-      qf[k][MR == 1 ? 0 : m] = w[k].x;
-      qf[k][MR == 1 ? 1 : 2 + m] = w[k].y;
+      for (int k = 0; k < KS; ++k) {
+        // A's registers: (row r, k lo), (row r + 8, k lo), (r, k hi), (r + 8, k hi)
+        qf[k][MR == 1 ? 0 : m] = w[k].x;
+        qf[k][MR == 1 ? 1 : 2 + m] = w[k].y;
+      }
     }
   }
 
@@ -396,39 +457,71 @@ __global__ void __launch_bounds__(kCaThreads, (D == 128 && FMT == 0) || MR == 2 
 
     // S = Q K^T.  Consecutive products go to different sums (with two groups of
     // tokens, even and odd steps have their own), so none waits for the last one.
-    constexpr int kPar = NT == 2 && KS > 1 ? 2 : 1;
-    float s[NT][2 * MR], s2[NT][2 * MR];
+    float s[NT][2 * MR];
+    if constexpr (kBytes) {
+      // the codes as they are, against the two bytes of q: 256 hi + lo
+      int32_t acc[NT][MR][4];
 #pragma unroll
-    for (int u = 0; u < C::kPiecesK; ++u) {
-      uint32_t w[NT][4];
+      for (int u = 0; u < C::kPiecesK; ++u) {
+        uint32_t w[NT][4];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) lds<C::kPieceK>(kt + (k_at ^ (u & 1) * 64u) + (u >> 1) * 128 + 8 * j * C::kRow, w[j]);
-      constexpr int kSteps = C::kPieceK / C::kEs / 4;
+        for (int j = 0; j < NT; ++j) lds<C::kPieceK>(kt + (k_at ^ (u & 1) * 64u) + (u >> 1) * 128 + 8 * j * C::kRow, w[j]);
+        constexpr int kSteps = kWords > 1 ? kWords / 2 : 1;
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        const int step = u * kSteps + k;
+        for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          uint32_t b0, b1;
-          if constexpr (FMT == 0) {
-            b0 = w[j][2 * k];
-            b1 = w[j][2 * k + 1];
-          } else {
-            codes_to_half<FMT>(w[j][k], b0, b1);
-          }
-          float* to = kPar == 2 && (step & 1) ? s2[j] : s[j];
-          if (step < kPar)
-            mma16<kHalf, kTop, true>(to, qf[step], b0, b1);
-          else
-            mma16<kHalf, kTop, false>(to, qf[step], b0, b1);
-        }
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int v = 0; v < MR; ++v) {
+              const uint32_t b1 = kWords > 1 ? w[j][2 * k + 1] : 0;
+              if (u + k == 0)
+                mma_s8<true>(acc[j][v], qb[0][v], w[j][0], b1);
+              else
+                mma_s8<false>(acc[j][v], qb[u * kSteps + k][v], w[j][2 * k], b1);
+            }
       }
-    }
-    if constexpr (kPar == 2) {
+      // |hi . k| <= 127 * 128 * d: the sum stays below 2^30
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 2 * MR; ++e) s[j][e] += s2[j][e];
+        for (int e = 0; e < 2 * MR; ++e)
+          s[j][e] = static_cast<float>(MR == 1 ? acc[j][0][e] * 256 + acc[j][0][2 + e]
+                                               : acc[j][0][e] * 256 + acc[j][MR - 1][e]);
+    } else {
+      constexpr int kPar = NT == 2 && KS > 1 ? 2 : 1;
+      float s2[NT][2 * MR];
+#pragma unroll
+      for (int u = 0; u < C::kPiecesK; ++u) {
+        uint32_t w[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) lds<C::kPieceK>(kt + (k_at ^ (u & 1) * 64u) + (u >> 1) * 128 + 8 * j * C::kRow, w[j]);
+        constexpr int kSteps = C::kPieceK / C::kEs / 4;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          const int step = u * kSteps + k;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            uint32_t b0, b1;
+            if constexpr (FMT == 0) {
+              b0 = w[j][2 * k];
+              b1 = w[j][2 * k + 1];
+            } else {
+              codes_to_half<FMT>(w[j][k], b0, b1);
+            }
+            float* to = kPar == 2 && (step & 1) ? s2[j] : s[j];
+            if (step < kPar)
+              mma16<kHalf, kTop, true>(to, qf[step], b0, b1);
+            else
+              mma16<kHalf, kTop, false>(to, qf[step], b0, b1);
+          }
+        }
+      }
+      if constexpr (kPar == 2) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2 * MR; ++e) s[j][e] += s2[j][e];
+      }
     }
 
     // scores, masks, running maxima

@@ -63,7 +63,12 @@ def compare(q, out, k, v, keys, dtype, fmt, what=""):
     """One sequence's heads against float64 over the listed keys."""
     k, v = np.nan_to_num(k), np.nan_to_num(v)
     ref, mag, top = attend(f64(q), k, v, keys)
-    tol = np.abs(ref) * half_step(dtype) + mag * attention_slack(q.shape[-1], len(keys), top)
+    rel = attention_slack(q.shape[-1], len(keys), top)
+    if dtype == "bf16" and fmt == "i8" and len(keys):
+        # q as 16-bit integers: each element off by at most 2^-15 of its head's largest, so a score by
+        # that times sum |k| / sqrt(d), and a probability's numerator and denominator by it each
+        rel = rel + 2 * 2.0 ** -15 * np.abs(f64(q)).max(-1, keepdims=True) * np.abs(k[:, keys]).sum(-1).max() / np.sqrt(q.shape[-1])
+    tol = np.abs(ref) * half_step(dtype) + mag * rel
     if dtype == "bf16":
         tol = tol + mag * (2.0 ** -8 if fmt == "native" else 2.0 ** -11) * (1 + 2.0 ** -8)
         if fmt != "native" and len(keys):
