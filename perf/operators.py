@@ -179,6 +179,8 @@ def _handles(s):
     s["cfg"] = binding.make_config(c["Hq"] * c["d"], 1, c["Hq"], c["Hkv"], conv_width=0, qk_mean=0, value_shift=0,
                                    rope_base=c.get("base", 0.0), dtype=binding.F32 if c["dtype"] == "f32" else binding.BF16)
     if c["op"] != "window":
+        # (the pool of a single sequence may have been gathered into another order of strides)
+        s["k"], s["v"] = s["k"].contiguous(), s["v"].contiguous()
         s["cache"] = device.DeviceKVCache.wrap(s["cfg"], s["k"], s["v"], s["len"], k_scale=s.get("k_scale"),
                                                v_scale=s.get("v_scale"), block_table=s.get("table"))
 
