@@ -19,24 +19,27 @@
 // TMEM columns: slots of 128 hold S, dP and, in each warp's own columns, the bf16
 // P and dS over them.  The dq pass has three: the scores of block k + 1 are computed
 // while block k is worked, S(k) in slot 2k mod 3 and dP(k) in slot 2k + 1 mod 3.  The
-// dkv pass has two, one for S and one for dP (dK and dV, 2 D columns, take the rest
-// at d = 128), and works a block as two halves of 64 columns with barriers of their
-// own: while eight warps form P and dS of one half the tensor core has the other
-// half's products (whole blocks in turn: 176 us at d = 128, the same 169 at d = 64).
-// The dq pass in halves was slower at d = 128 (134 us against 129).
+// dkv pass works a block as two halves of 64 columns, eight warps each, whose S and
+// dP share a slot: while P and dS of one half are formed the tensor core has the other
+// half's products (whole blocks in turn: 176 us against 152 at d = 128).  It has three
+// slots at d <= 64 (two: 14 us of 367 more in a training step of the second case
+// below), two at d = 128, where dK and dV take half of TMEM.  The dq pass in halves
+// was slower at d = 128 (134 us against 129).
 //
 // The dkv pass's work is cut evenly: the blocks of all key tiles, in order, are
 // shared out to one CTA per SM; a tile whose blocks end up in several CTAs leaves
 // fp32 partial sums that a third kernel adds in the order of the CTAs, so equal
 // calls give equal bits, windows and sinks of any shape fill the GPU, and only
-// the tiles at the cuts cost extra traffic.
+// the tiles at the cuts cost extra traffic.  A tile counts as its blocks and three
+// more for the loads and stores around them: by blocks alone the CTAs at the short
+// tiles of a sequence's end ran 20 % longer than the rest.
 //
-// Measured: 32 / 8 heads of 128, 4096 tokens, window 1024: dq 132 us, dkv 150 us and
-// 9 us for its join, 680 and 760 TFLOP/s of the products they form.  8 / 2 heads of
-// 64, 8192 tokens, window 4096: 116, 168 and 7 us, 670 and 590 TFLOP/s.  The bound is
+// Measured: 32 / 8 heads of 128, 4096 tokens, window 1024: dq 132 us, dkv 134 us and
+// 10 us for its join, 680 and 900 TFLOP/s of the products they form.  8 / 2 heads of
+// 64, 8192 tokens, window 4096: 117, 154 and 8 us, 660 and 670 TFLOP/s.  The bound is
 // the chain of each block, scores out of TMEM, exponentials and products, bf16 back
-// into TMEM: the tensor core is busy in 34 to 44 % of the cycles, the warps issue in
-// 33 to 46 %, memory is idle.  Both passes form the scores anew, 7 products where
+// into TMEM: the tensor core is busy in 34 to 51 % of the cycles, the warps issue in
+// 38 to 49 %, memory is idle.  Both passes form the scores anew, 7 products where
 // 5 would do, because one pass over both needs atomic sums of dq.
 //
 // No cluster multicast; every wait is bounded.

@@ -41,8 +41,11 @@
 // softmax's issue slots (16 warps an SM at 64 channels and 12 at 128 issue in half
 // of the cycles), not the memory.
 //
-// fp32 layers.  CUDA cores, fp32 throughout, chunks of four query heads: d / 4
-// lanes share a token, each with four channels.
+// fp32 layers.  CUDA cores, fp32 throughout, chunks of four query heads; see
+// F32Cfg for how a warp shares out its tokens.  32 sequences of 16384 tokens, 8 / 2
+// heads of 64, int8: 94 us, 1.4 TB/s; 16 of 8192, 32 / 8 heads of 128, e4m3: 190 us;
+// 32 of 8192 over an fp32 cache: 80 us, 3.4 TB/s.  The bound is instruction issue: a
+// code is multiplied by four heads in fp32, twice.
 //
 // Splits leave (numerators, max, sum) in the workspace and a second kernel
 // joins them; with one split the result is written at once.
@@ -50,6 +53,7 @@
 
 #include <algorithm>
 
+#include "attn_math.cuh"
 #include "cache_codes.cuh"
 #include "sm100.cuh"
 
@@ -709,16 +713,28 @@ __global__ void __launch_bounds__(kCaThreads, (D == 128 && FMT == 0) || MR == 2 
 }
 
 // ----------------------------------------------------------------- fp32
-// D / 4 lanes share a token; a warp works 16 tokens at a time.
+// A token is shared by LPK lanes of CL channels each, a warp works KPW tokens at
+// once, U times.  Codes: 16 channels, so that a lane's load is 16 bytes and a score
+// costs two or three shuffles (8 channels on three CTAs an SM: 115 us against 94; 4
+// channels: 300 us).  fp32 cache: 8, which leaves registers for the rows under way.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kCaThreads)
+struct F32Cfg {
+  static constexpr int CL = D == 16 || FMT == 0 ? 8 : 16, LPK = D / CL, KPW = 32 / LPK;
+  static constexpr int kSteps = 16 / KPW, U = kSteps < 2 ? kSteps : 2, kBatches = kSteps / U;   // of a tile of 16 tokens
+  static constexpr int kVecs = FMT == 0 ? 2 : 1;   // loads of a lane's channels
+};
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kCaThreads, FMT == 0 ? 3 : 2)
     cache_attn_f32_kernel(const CacheAttnArgs a) {
   pdl_enter();
-  constexpr int LPK = D / 4, KPW = 32 / LPK, H = kCacheAttnHeadsF32;
-  constexpr int kSteps = 16 / KPW, U = kSteps < 8 ? kSteps : 8;   // tokens a lane group holds at once
+  using C = F32Cfg<D, FMT>;
+  constexpr int CL = C::CL, LPK = C::LPK, KPW = C::KPW, U = C::U, H = kCacheAttnHeadsF32;
   __shared__ float num[kWarps * KPW][H][D];
   __shared__ float ml[kWarps * KPW][H][2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / LPK, e0 = lane % LPK * 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / LPK, sub = lane % LPK;
+  // channels of a lane, in fours: fp32 rows are shared out in 16-byte pieces in turn
+  auto chan = [&](int i) { return FMT == 0 ? (i * LPK + sub) * 4 : sub * CL + i * 4; };
   const int chunks = (a.G + H - 1) / H;
   const int unit = blockIdx.x / a.splits, sp = blockIdx.x - unit * a.splits;
   const int hc = unit % chunks, g = unit / chunks % a.Hkv, b = unit / chunks / a.Hkv;
@@ -727,100 +743,168 @@ __global__ void __launch_bounds__(kCaThreads)
   const Visible<16> vis(L, a.window, a.sinks);
   const int i0 = static_cast<int>(static_cast<int64_t>(vis.n) * sp / a.splits);
   const int i1 = static_cast<int>(static_cast<int64_t>(vis.n) * (sp + 1) / a.splits);
-  float q[H][4], o[H][4], m[H], l[H];
+  float2 q[H][CL / 2], o[H][CL / 2];
+  float m[H], l[H];
 #pragma unroll
   for (int h = 0; h < H; ++h) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (h < heads)
-      x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.Hq + h0 + h) * D + e0);
-    q[h][0] = x.x;
-    q[h][1] = x.y;
-    q[h][2] = x.z;
-    q[h][3] = x.w;
+#pragma unroll
+    for (int i = 0; i < CL / 4; ++i) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (h < heads)
+        x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.Hq + h0 + h) * D + chan(i));
+      q[h][2 * i] = make_float2(x.x, x.y);
+      q[h][2 * i + 1] = make_float2(x.z, x.w);
+      o[h][2 * i] = o[h][2 * i + 1] = make_float2(0.f, 0.f);
+    }
     m[h] = -INFINITY;
-    l[h] = o[h][0] = o[h][1] = o[h][2] = o[h][3] = 0.f;
+    l[h] = 0.f;
   }
   const float cs = kLog2eC * rsqrtf(static_cast<float>(D));
-  auto fetch = [&](const void* base, int64_t row, float (&x)[4]) {
-    if constexpr (FMT == 0) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + row * D + e0));
-      x[0] = v.x;
-      x[1] = v.y;
-      x[2] = v.z;
-      x[3] = v.w;
-    } else {
-      const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(base) + row * D + e0));
-      float y[8];
-      decode8<FMT>(make_uint2(w, 0), y);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = y[e];
-    }
+
+  // ---- what is read of U tokens; batch n: tile i0 + warp + n / kBatches * kWarps
+  struct Raw {
+    uint4 k[U][C::kVecs], v[U][C::kVecs];
+    float sk, sv;
+    unsigned on;
   };
-  for (int i = i0 + warp; i < i1; i += kWarps) {
-    const int t0 = vis.start(i);
-    const int64_t rb = row_of(a, b, g, t0);
+  auto tile_of = [&](int n) { return i0 + warp + n / C::kBatches * kWarps; };
+  auto locate = [&](int n) {
+    const int i = tile_of(n);
+    return i < i1 ? row_of(a, b, g, vis.start(i)) : 0;
+  };
+  auto load = [&](int n, int64_t rb, Raw& x) {
+    const int i = tile_of(n);
+    x.on = 0;
+    x.sk = cs;
+    x.sv = 1.f;
+    if (i >= i1) return;
     if (rb < 0) {
       if (lane == 0) raise_dev_err(a.dev_err, CCGQA_DEVERR_INDEX);
-      continue;
+      return;
     }
-    const float sk = FMT == 0 ? cs : cs * __ldcg(a.k_scale + (rb >> a.block_shift));
-    const float sv = FMT == 0 ? 1.f : __ldcg(a.v_scale + (rb >> a.block_shift));
+    if (FMT != 0) {
+      x.sk = cs * __ldcg(a.k_scale + (rb >> a.block_shift));
+      x.sv = __ldcg(a.v_scale + (rb >> a.block_shift));
+    }
+    const int t0 = vis.start(i);
 #pragma unroll
-    for (int u0 = 0; u0 < kSteps; u0 += U) {
-      float k[U][4], v[U][4];
-      bool on[U];
+    for (int u = 0; u < U; ++u) {
+      const int t = (n % C::kBatches * U + u) * KPW + grp;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = (u0 + u) * KPW + grp;
-        on[u] = vis.sees(t0 + t);
+      for (int w = 0; w < C::kVecs; ++w) x.k[u][w] = make_uint4(0, 0, 0, 0);   // of a token that is not seen
+      if (!vis.sees(t0 + t)) continue;
+      x.on |= 1u << u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) k[u][e] = v[u][e] = 0.f;
-        if (on[u]) {
-          fetch(a.ck, rb + t, k[u]);
-          fetch(a.cv, rb + t, v[u]);
+      for (int w = 0; w < C::kVecs; ++w) {
+        const int64_t at = ((rb + t) * D + (FMT == 0 ? chan(w) : sub * CL)) * (FMT == 0 ? 4 : 1);
+        const char* ck = static_cast<const char*>(a.ck) + at;
+        const char* cv = static_cast<const char*>(a.cv) + at;
+        if constexpr (FMT != 0 && CL == 8) {
+          const uint2 y = __ldcg(reinterpret_cast<const uint2*>(ck)), z = __ldcg(reinterpret_cast<const uint2*>(cv));
+          x.k[u][w] = make_uint4(y.x, y.y, 0, 0);
+          x.v[u][w] = make_uint4(z.x, z.y, 0, 0);
+        } else {
+          x.k[u][w] = __ldcg(reinterpret_cast<const uint4*>(ck));
+          x.v[u][w] = __ldcg(reinterpret_cast<const uint4*>(cv));
         }
       }
+    }
+  };
+  auto values = [&](const uint4 (&r)[C::kVecs], float2 (&y)[CL / 2]) {
+    if constexpr (FMT == 0) {
+#pragma unroll
+      for (int w = 0; w < C::kVecs; ++w) {
+        y[2 * w] = make_float2(__uint_as_float(r[w].x), __uint_as_float(r[w].y));
+        y[2 * w + 1] = make_float2(__uint_as_float(r[w].z), __uint_as_float(r[w].w));
+      }
+    } else {
+#pragma unroll
+      for (int w = 0; w < CL / 8; ++w) {
+        float x[8];
+        decode8<FMT>(w ? make_uint2(r[0].z, r[0].w) : make_uint2(r[0].x, r[0].y), x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[4 * w + e] = make_float2(x[2 * e], x[2 * e + 1]);
+      }
+    }
+  };
+  auto work = [&](const Raw& r) {
+    float x[H][U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float2 k[CL / 2];
+      values(r.k[u], k);
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        float x[U], top = m[h];
+        float2 y = fmul2(q[h][0], k[0]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          x[u] = q[h][0] * k[u][0];
+        for (int e = 1; e < CL / 2; ++e) y = ffma2(q[h][e], k[e], y);
+        x[h][u] = y.x + y.y;
+      }
+    }
 #pragma unroll
-          for (int e = 1; e < 4; ++e) x[u] = fmaf(q[h][e], k[u][e], x[u]);
-        }
+    for (int off = LPK / 2; off > 0; off >>= 1)
 #pragma unroll
-        for (int off = LPK / 2; off > 0; off >>= 1)
+      for (int h = 0; h < H; ++h)
 #pragma unroll
-          for (int u = 0; u < U; ++u) x[u] += __shfl_xor_sync(0xffffffffu, x[u], off);
+        for (int u = 0; u < U; ++u) x[h][u] += __shfl_xor_sync(0xffffffffu, x[h][u], off);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          x[u] = on[u] ? x[u] * sk : -INFINITY;
-          top = fmaxf(top, x[u]);
-        }
-        const float base = finite_or_zero(top);
+    for (int h = 0; h < H; ++h) {
+      float top = m[h];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        x[h][u] = (r.on >> u) & 1 ? x[h][u] * r.sk : -INFINITY;
+        top = fmaxf(top, x[h][u]);
+      }
+      const float base = finite_or_zero(top);
+      if (top > m[h]) {
         const float f = exp2f(finite_or_zero(m[h]) - base);   // sums are zero while there is no max
         m[h] = top;
         l[h] *= f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[h][e] *= f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (!on[u]) continue;
-          const float p = exp2f(x[u] - base), w = p * sv;
-          l[h] += p;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[h][e] = fmaf(w, v[u][e], o[h][e]);
-        }
+        for (int e = 0; e < CL / 2; ++e) o[h][e] = fmul2(o[h][e], make_float2(f, f));
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float p = (r.on >> u) & 1 ? exp2f(x[h][u] - base) : 0.f;
+        l[h] += p;
+        x[h][u] = p * r.sv;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!((r.on >> u) & 1)) continue;
+      float2 v[CL / 2];
+      values(r.v[u], v);
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int e = 0; e < CL / 2; ++e) o[h][e] = ffma2(make_float2(x[h][u], x[h][u]), v[e], o[h][e]);
+    }
+  };
+  // two batches of rows: one is worked while the next is on its way, and the page of
+  // the one after is looked up
+  const int n = i1 > i0 + warp ? ((i1 - i0 - warp + kWarps - 1) / kWarps) * C::kBatches : 0;
+  if (n > 0) {
+    Raw r0, r1;
+    load(0, locate(0), r0);
+    int64_t rb = locate(1);
+    for (int i = 0; i < n; i += 2) {
+      load(i + 1, rb, r1);
+      rb = locate(i + 2);
+      work(r0);
+      load(i + 2, rb, r0);
+      rb = locate(i + 3);
+      if (i + 1 < n) work(r1);
     }
   }
   // ---- join the lane groups
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const int row = warp * KPW + grp;
-    *reinterpret_cast<float4*>(&num[row][h][e0]) = make_float4(o[h][0], o[h][1], o[h][2], o[h][3]);
-    if (e0 == 0) {
+#pragma unroll
+    for (int i = 0; i < CL / 4; ++i)
+      *reinterpret_cast<float4*>(&num[row][h][chan(i)]) = make_float4(o[h][2 * i].x, o[h][2 * i].y, o[h][2 * i + 1].x, o[h][2 * i + 1].y);
+    if (sub == 0) {
       ml[row][h][0] = l[h] == 0.f ? -INFINITY : finite_or_zero(m[h]);
       ml[row][h][1] = l[h];
     }

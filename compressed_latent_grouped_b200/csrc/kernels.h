@@ -289,7 +289,7 @@ int cache_attn_splits(int64_t units, int64_t keys, int ctas_per_sm);
 constexpr int kCacheAttnMaxCtas = 4;      // on an SM
 // What launch_bounds asks for: registers and shared memory (fp32: registers alone).
 constexpr int cache_attn_ctas(int d, int fmt, int G, bool f32) {
-  return f32 ? 3 : ((d == 128 && fmt == 0) || G > 8 ? 2 : (d == 128 ? 3 : kCacheAttnMaxCtas));
+  return f32 ? (fmt == 0 ? 3 : 2) : ((d == 128 && fmt == 0) || G > 8 ? 2 : (d == 128 ? 3 : kCacheAttnMaxCtas));
 }
 template <typename T>
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int fmt, cudaStream_t stream);
