@@ -1,7 +1,7 @@
 // C ABI of the operators on finished query / key / value rows: the append with
 // the rotation, the cache read-back, the one-token attention over the cache and
-// the window attention of whole sequences with its gradients.  Host-side validation and dispatch, as in api.cu: nothing is launched on a bad
-// argument.
+// the window attention of whole sequences with its gradients.  Host-side validation
+// and dispatch, as in api.cu: nothing is launched on a bad argument.
 #include <algorithm>
 
 #include "api_internal.h"
@@ -38,8 +38,12 @@ int log2_of(int x) {
   return s;
 }
 
-// Validate the 8-bit description of a cache (null: the working type).
-ccgqa_status check_cache8(const ccgqa_kvcache* c, const ccgqa_cache8* c8) {
+// Validate a cache and its 8-bit description (null: the working type).
+ccgqa_status check_cache8(const Geo& g, const ccgqa_kvcache* c, const ccgqa_cache8* c8) {
+  const ccgqa_status s = check_cache(g, c, false);
+  if (s != CCGQA_OK) return s;
+  // the kernels round token counts up to tiles of at most 128 in 32 bits
+  if (c->cap > INT32_MAX - 128) return CCGQA_ERR_UNSUPPORTED;
   if (!c8) return CCGQA_OK;
   if (c8->format != CCGQA_CACHE_I8 && c8->format != CCGQA_CACHE_E4M3) return CCGQA_ERR_INVALID_ARG;
   const int b = c8->block;
@@ -188,8 +192,7 @@ CCGQA_API ccgqa_status ccgqa_kvcache_append_rope(const ccgqa_config* cfg,
   Geo g;
   ccgqa_status s = derive(cfg, &g);
   if (s != CCGQA_OK) return s;
-  if ((s = check_cache(g, cache, false)) != CCGQA_OK) return s;
-  if ((s = check_cache8(cache, c8)) != CCGQA_OK) return s;
+  if ((s = check_cache8(g, cache, c8)) != CCGQA_OK) return s;
   if (!a || a->n_new < 0) return CCGQA_ERR_INVALID_ARG;
   if (a->n_new > cache->cap) return CCGQA_ERR_CAPACITY;
   if (a->n_new == 0) return CCGQA_OK;
@@ -214,8 +217,7 @@ CCGQA_API ccgqa_status ccgqa_kvcache_read(const ccgqa_config* cfg, const ccgqa_k
   Geo g;
   ccgqa_status s = derive(cfg, &g);
   if (s != CCGQA_OK) return s;
-  if ((s = check_cache(g, cache, false)) != CCGQA_OK) return s;
-  if ((s = check_cache8(cache, c8)) != CCGQA_OK) return s;
+  if ((s = check_cache8(g, cache, c8)) != CCGQA_OK) return s;
   if (first < 0 || n < 0) return CCGQA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(first) + n > cache->cap) return CCGQA_ERR_CAPACITY;
   if (n == 0) return CCGQA_OK;
@@ -264,8 +266,7 @@ CCGQA_API ccgqa_status ccgqa_cache_attention(const ccgqa_config* cfg, const ccgq
   Geo g;
   ccgqa_status s = derive(cfg, &g);
   if (s != CCGQA_OK) return s;
-  if ((s = check_cache(g, cache, false)) != CCGQA_OK) return s;
-  if ((s = check_cache8(cache, c8)) != CCGQA_OK) return s;
+  if ((s = check_cache8(g, cache, c8)) != CCGQA_OK) return s;
   if (!window_ok(win) || !q || !out || !aligned16(q) || !aligned16(out)) return CCGQA_ERR_INVALID_ARG;
   const int64_t units = attn_units(g, cache->batch);
   if (units > 0x7fffffff / kCacheAttnMaxSplits) return CCGQA_ERR_UNSUPPORTED;

@@ -777,6 +777,10 @@ __global__ void __launch_bounds__(kCaThreads, FMT == 0 ? 3 : 2)
     x.on = 0;
     x.sk = cs;
     x.sv = 1.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int w = 0; w < C::kVecs; ++w) x.k[u][w] = make_uint4(0, 0, 0, 0);   // of tokens that are not seen
     if (i >= i1) return;
     if (rb < 0) {
       if (lane == 0) raise_dev_err(a.dev_err, CCGQA_DEVERR_INDEX);
@@ -790,8 +794,6 @@ __global__ void __launch_bounds__(kCaThreads, FMT == 0 ? 3 : 2)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int t = (n % C::kBatches * U + u) * KPW + grp;
-#pragma unroll
-      for (int w = 0; w < C::kVecs; ++w) x.k[u][w] = make_uint4(0, 0, 0, 0);   // of a token that is not seen
       if (!vis.sees(t0 + t)) continue;
       x.on |= 1u << u;
 #pragma unroll

@@ -277,7 +277,8 @@ class DeviceKVCache:
 
     The handle keeps pointers, so the tensors must stay where they are; it
     keeps nothing of their contents.  Calls run on ``stream`` (default: the
-    current stream of the cache's device)."""
+    current stream of the cache's device); appends to one cache run one after
+    another, as what they write and read requires."""
 
     FORMATS = {"i8": (B.CACHE_I8, torch.int8), "e4m3": (B.CACHE_E4M3, torch.float8_e4m3fn)}
 
@@ -336,7 +337,7 @@ class DeviceKVCache:
         _check_dense(where, "len", len_, (self.batch,), torch.int32, self.device)
         self.block, self.cache8 = 0, None
         if fmt:
-            if k_scale is None or k_scale.dim() != 3 or not k_scale.shape[2] or k.shape[2] % k_scale.shape[2]:
+            if k_scale is None or k_scale.dim() != 3 or not k_scale.shape[2] or not k.shape[2] or k.shape[2] % k_scale.shape[2]:
                 _bad(where, "an 8-bit cache needs scales [..., Hkv, tokens / block]")
             self.block = k.shape[2] // k_scale.shape[2]
             sshape = (*shape[:2], shape[2] // self.block)

@@ -316,6 +316,7 @@ CCGQA_API ccgqa_status ccgqa_output_projection(const ccgqa_config* cfg, const vo
  * sequences over a sliding window with its gradients.
  * Of cfg they use E, C, n_q_heads, n_kv_heads (head dim d = E / (C Hq)), dtype
  * and, where stated, rope_base and causal; cfg is validated as for every call.
+ * A cache holds at most 2^31 - 129 tokens per sequence (CCGQA_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------- */
 
 /* A tensor of head rows [batch, tokens, heads, d]: element (b, t, h, e) lies at
@@ -378,7 +379,8 @@ typedef struct {
   const int32_t* pos;
   int32_t* tickets;   /* nullable, [batch], zero before the first call, zero after each:
                          with it the append is one launch (its last CTA that has
-                         read a length moves it on), without it two */
+                         read a length moves it on), without it two.  Appends to
+                         one cache run one after another, with or without it. */
 } ccgqa_append;
 CCGQA_API ccgqa_status ccgqa_kvcache_append_rope(const ccgqa_config* cfg,
                                                  const ccgqa_kvcache* cache,

@@ -163,3 +163,14 @@ class _At:
 
     def element_size(self):
         return 1
+
+
+@pytest.mark.parametrize("cap,ok", [(2 ** 31 - 1, False), (2 ** 31 - 128, False), (2 ** 31 - 129, True)])
+def test_longest_cache(lib, cap, ok):
+    """Token counts are rounded up to tiles in 32 bits: a longer cache is refused."""
+    cfg, c = config(8, 2, 64), _cache(cap=cap)
+    assert _append(lib, cfg, c, n=0) == (0 if ok else 2)
+    assert B.ccgqa_kvcache_read(cfg, c, None, 0, 0, rows(), rows(), stream=0, check=False) == (0 if ok else 2)
+    s = lib.ccgqa_cache_attention(ctypes.byref(cfg), None, ctypes.byref(c), None, P, P, None, 0, None, None)
+    assert s == (4 if ok else 2)
+    assert B.ccgqa_launch_count() == 0
