@@ -279,3 +279,40 @@ def test_a_chunk_then_tokens(fmt, page):
             ref = rotate(f64(q[b, t:t + 1]), [lens[b] - 1], base)
             assert_within(f64(qt[b]), ref, np.abs(ref) * 2.0 ** -8 + 1e-5, "query")
     assert c.error_bits() == 0
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("fmt", ["native", "i8", "e4m3"])
+@pytest.mark.parametrize("page,window,sinks", [(0, 0, 0), (16, 0, 0), (64, 301, 20)])
+def test_fp32_layers(d, fmt, page, window, sinks):
+    """Lengths around a warp's, a tile's and a split's share of the tokens; groups that fill a chunk of heads and do not."""
+    Hq, Hkv = (4, 1) if page == 0 else (14, 2)
+    block = {"native": 0, "i8": 16, "e4m3": 16 if page == 16 else 64}[fmt]
+    lens = (0, 1, 15, 16, 17, 63, 65, 128, 1023, 2047, 2048)
+    c, table, q = make(Hq, Hkv, d, "f32", fmt, block, 2048, page, lens, seed=d)
+    poison(c, table, lens, window, sinks)
+    out = c.attend(q, window=window, sinks=sinks)
+    again = c.attend(q, out=torch.full_like(q, 7.0), window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert c.error_bits() == 0
+    assert torch.equal(out, again), "equal calls, other bits"
+    check(c, table, q, out, lens, window, sinks, "f32", fmt)
+
+
+@pytest.mark.parametrize("fmt", ["native", "e4m3"])
+def test_fp32_layers_and_bad_pages(fmt):
+    """Pages that are not in the pool count as absent, beside pages that are."""
+    lens = (400, 77)
+    c, table, q = make(8, 2, 64, "f32", fmt, 16 if fmt == "e4m3" else 0, 512, 16, lens)
+    good = table.clone()
+    table[0, 3] = -1
+    table[0, 24] = c.k.shape[0]
+    table[1, 4] = 1 << 30
+    out = c.attend(q)
+    torch.cuda.synchronize()
+    assert c.error_bits() == B.DEVERR_INDEX
+    k, v = cache_values(c, good)
+    for b, L in enumerate(lens):
+        gone = {0: (3, 24), 1: (4,)}[b]
+        keys = np.array([t for t in range(L) if t // 16 not in gone])
+        compare(q[b], out[b], k[b], v[b], keys, "f32", fmt, f"sequence {b}")

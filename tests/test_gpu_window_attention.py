@@ -314,3 +314,28 @@ def test_python_refusals():
     assert B.ccgqa_launch_count() == n
     with pytest.raises(RuntimeError):
         window_attention(cfg, q.cpu(), k.cpu(), v.cpu())
+
+
+@pytest.mark.parametrize("Bn,S,Hq,Hkv,d,window,sinks", [
+    (1, 2048, 16, 4, 64, 0, 0),          # tiles of very different length
+    (2, 1900, 16, 4, 128, 700, 5),       # a tile's partial sums in two CTAs
+    (1, 2500, 16, 4, 32, 1000, 200),     # every query sees the first tile and a half
+    (5, 700, 16, 2, 64, 65, 0),          # short tiles, several of them in a CTA
+    (3, 900, 12, 4, 32, 0, 0),
+    (2, 1300, 10, 2, 128, 0, 0),         # groups of five: rows left over in every block
+])
+def test_gradients_of_shared_out_tiles(Bn, S, Hq, Hkv, d, window, sinks):
+    """Enough blocks that tiles are cut across CTAs and CTAs take several tiles."""
+    cfg = config(Hq, Hkv, d)
+    q, k, v, do = inputs(Bn, S, Hq, Hkv, d, "bf16", seed=7, layout="packed")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(window=window, sinks=sinks, dev_err=err)
+    ref, tol = reference(q, k, v, window, sinks, do)
+    out, stats = window_attention(cfg, q, k, v, with_stats=True, **kw)
+    close(out, ref["out"], tol["out"], "out")
+    got = window_attention_backward(cfg, q, k, v, out, stats, do, **kw)
+    again = window_attention_backward(cfg, q, k, v, out, stats, do, **kw)
+    for m, x, y in zip(("dq", "dk", "dv"), got, again):
+        close(x, ref[m], tol[m], m)
+        assert torch.equal(x, y), f"{m}: equal calls, other bits"
+    assert int(err) == 0
