@@ -339,3 +339,23 @@ def test_gradients_of_shared_out_tiles(Bn, S, Hq, Hkv, d, window, sinks):
         close(x, ref[m], tol[m], m)
         assert torch.equal(x, y), f"{m}: equal calls, other bits"
     assert int(err) == 0
+
+
+@pytest.mark.parametrize("Bn,S,Hq,Hkv,d,window,sinks", [
+    (1, 89, 8, 2, 64, 0, 0),             # one tile per head, of three blocks
+    (3, 383, 6, 3, 32, 20, 0),           # more tiles than shares of two blocks
+    (40, 300, 4, 4, 128, 60, 0),         # several whole tiles in a CTA
+    (70, 130, 8, 2, 32, 0, 0),
+])
+def test_gradients_of_whole_tiles(Bn, S, Hq, Hkv, d, window, sinks):
+    """Tiles too short to be cut: each in one CTA, no sums to join."""
+    cfg = config(Hq, Hkv, d)
+    q, k, v, do = inputs(Bn, S, Hq, Hkv, d, "bf16", seed=11)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(window=window, sinks=sinks, dev_err=err)
+    ref, tol = reference(q, k, v, window, sinks, do)
+    out, stats = window_attention(cfg, q, k, v, with_stats=True, **kw)
+    got = window_attention_backward(cfg, q, k, v, out, stats, do, **kw)
+    for m, x in zip(("dq", "dk", "dv"), got):
+        close(x, ref[m], tol[m], m)
+    assert int(err) == 0
