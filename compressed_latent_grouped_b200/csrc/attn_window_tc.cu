@@ -7,7 +7,8 @@
 // Query rows are packed per kv group as in the causal kernel: row r of a tile is
 // position t0 + r / G, head g G + r % G, gathered by a 5-D TMA box from any
 // strides; a tile holds floor(128 / G) positions, rows past them are zeroed
-// once.  One CTA owns T (one to three) consecutive query tiles of one kv group and walks the
+// once.  One CTA owns T (one to three; one of the tiles left over by whole rounds)
+// consecutive query tiles of one kv group and walks the
 // key pieces (64 keys) they see: the sinks' pieces, then the window's, whose first
 // key is the first one any of its rows sees: a TMA box may start at any row, so
 // a window of W keys costs W + (positions of the CTA) keys rounded up to 64, not
@@ -77,7 +78,7 @@ template <int D, int T>
 __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, FwdCfg<D, T>::kCtas)
     window_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WindowArgs a,
-                         int n_groups) {
+                         int n_groups, int n_alone) {
   pdl_enter();
   using C = FwdCfg<D, T>;
   extern __shared__ uint8_t smem_raw[];
@@ -94,12 +95,14 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, FwdCfg<D, T>::kCtas)
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const int G = a.G, BH = a.B * a.Hkv;
-  const int grp = n_groups - 1 - static_cast<int>(blockIdx.x) / BH;   // the longest first
+  // groups of kTiles tiles, the longest first, then the first n_alone tiles by themselves
+  const int grp = n_groups - 1 - static_cast<int>(blockIdx.x) / BH;
   const int bg = static_cast<int>(blockIdx.x) % BH;
   const int b = bg / a.Hkv, g = bg % a.Hkv;
   const int pos = 128 / G, rows_used = pos * G;
-  const int t0 = grp * C::kTiles * pos;
-  const int t_last = min(t0 + C::kTiles * pos, a.S) - 1;
+  const int tiles = C::kTiles == 1 || grp < 0 ? 1 : C::kTiles;
+  const int t0 = (n_alone + grp * tiles) * pos;
+  const int t_last = min(t0 + tiles * pos, a.S) - 1;
   const int lo = max(0, t0 - a.window + 1);      // first key of the window of any row
   const int sinks = min(a.sinks, lo);            // sink keys before it
   const int n_sink = (sinks + kPiece - 1) / kPiece;
@@ -110,14 +113,14 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, FwdCfg<D, T>::kCtas)
     mbar_init(q_full, 1);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], C::kTiles);
+      mbar_init(&kv_empty[s], tiles);
     }
     for (int i = 0; i < 2 * C::kTiles; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 128);
       mbar_init(&o_done[i], 1);
     }
-    mbar_init(drain, C::kTiles);
+    mbar_init(drain, tiles);
     abort_flag = 0;
     fence_barrier_init();
   }
@@ -137,9 +140,8 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, FwdCfg<D, T>::kCtas)
       prefetch_tensormap(&tmQ);
       prefetch_tensormap(&tmK);
       prefetch_tensormap(&tmV);
-      mbar_arrive_expect_tx(q_full, C::kTiles * rows_used * D * 2);
-#pragma unroll
-      for (int x = 0; x < C::kTiles; ++x)
+      mbar_arrive_expect_tx(q_full, tiles * rows_used * D * 2);
+      for (int x = 0; x < tiles; ++x)
 #pragma unroll
         for (int p = 0; p < C::kPanels; ++p)
           tma_load_5d(smem + C::kOffQ + x * C::kTileBytes + p * C::kPanelQ, &tmQ, q_full, p * C::kPanelCols, 0, g,
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, FwdCfg<D, T>::kCtas)
         }
       }
     }
-  } else if (warp >= 1 && warp <= C::kTiles) {
+  } else if (warp >= 1 && warp <= tiles) {
     // ------------------------------------------------------------ MMA issuers
     if (elect_one()) {
       const int x = warp - 1;
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, FwdCfg<D, T>::kCtas)
         }
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 4 + 4 * tiles) {
     // ------------------------------------------------------------ softmax
     const int x = (warp - 4) >> 2;
     const int q4 = warp & 3;
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, FwdCfg<D, T>::kCtas)
     }
   }
 
-  if (abort_flag && warp >= 1 && warp <= C::kTiles && elect_one()) drain_mmas(drain);
+  if (abort_flag && warp >= 1 && warp <= tiles && elect_one()) drain_mmas(drain);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -362,14 +364,23 @@ cudaError_t launch_fwd(const WindowArgs& a, cudaStream_t stream) {
   if (!packed_rows_map(&tmQ, a.q, a, 128 / a.G) || !key_rows_map(&tmK, a.k, a, kPiece) ||
       !key_rows_map(&tmV, a.v, a, kPiece))
     return cudaErrorInvalidValue;
-  const int per_cta = C::kTiles * (128 / a.G);
-  const int64_t n_groups = (a.S + per_cta - 1) / per_cta;
-  const int64_t grid = n_groups * a.B * a.Hkv;
+  // Groups for whole rounds of the GPU; where a CTA per SM is enough for the tiles
+  // left over, one tile in each (16 / 4 heads of 32, 8192 tokens, window 1024: 64 us,
+  // 70 in groups alone; window 512: 45 and 49; 32 / 8 heads of 128, 4096 tokens,
+  // window 1024, with statistics: 88 and 90).  Not with windows so wide that the first
+  // tiles, which come last, are short anyway (the last case with a window of 2048:
+  // 121 us, 119 in groups).
+  const int64_t BH = static_cast<int64_t>(a.B) * a.Hkv, n_tiles = (a.S + 128 / a.G - 1) / (128 / a.G);
+  const int64_t full = n_tiles * BH / (C::kTiles * sm_count()) * sm_count() / BH;
+  int64_t n_alone = n_tiles - C::kTiles * full;
+  if (C::kTiles == 1 || full == 0 || n_alone * BH > sm_count() || a.window > a.S / 4) n_alone = 0;
+  const int64_t n_groups = (n_tiles - n_alone + C::kTiles - 1) / C::kTiles;
+  const int64_t grid = (n_groups + n_alone) * BH;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_fwd_tc_kernel<D, T>), static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
   e = launch_pdl(window_fwd_tc_kernel<D, T>, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), C::kSmem, stream, tmQ,
-                 tmK, tmV, a, static_cast<int>(n_groups));
+                 tmK, tmV, a, static_cast<int>(n_groups), static_cast<int>(n_alone));
   if (e != cudaSuccess) return e;
   count_launches(1);
   return cudaGetLastError();

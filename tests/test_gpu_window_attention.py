@@ -359,3 +359,29 @@ def test_gradients_of_whole_tiles(Bn, S, Hq, Hkv, d, window, sinks):
     for m, x in zip(("dq", "dk", "dv"), got):
         close(x, ref[m], tol[m], m)
     assert int(err) == 0
+
+
+@pytest.mark.parametrize("Bn,S,Hq,Hkv,d,window,sinks", [
+    (1, 2500, 128, 16, 128, 300, 0),     # pairs of tiles for one round, the rest by themselves
+    (2, 1800, 40, 20, 128, 77, 9),
+    (1, 3601, 64, 16, 32, 250, 3),       # threes of tiles
+    (3, 1501, 45, 9, 32, 130, 0),        # groups of five: rows left over in every tile
+])
+def test_tiles_left_over(Bn, S, Hq, Hkv, d, window, sinks):
+    """More query tiles than whole rounds of the GPU hold; a few heads of each group against float64."""
+    cfg = config(Hq, Hkv, d)
+    q, k, v, _ = inputs(Bn, S, Hq, Hkv, d, "bf16", seed=3)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = window_attention(cfg, q, k, v, window=window, sinks=sinks, dev_err=err)
+    assert int(err) == 0
+    G = Hq // Hkv
+    for g in {0, Hkv // 2, Hkv - 1}:
+        for h in {g * G, g * G + G - 1}:
+            ref, tol = reference(q[:, :, h:h + 1], k[:, :, g:g + 1], v[:, :, g:g + 1], window, sinks)
+            close(out[:, :, h:h + 1], ref["out"], tol["out"], f"head {h}")
+    ok = visible(S, window, sinks)               # and every row is some mean of values it sees
+    top = torch.stack([v[b, :, :].float().abs().amax(-1) for b in range(Bn)])
+    for b in range(Bn):
+        for g in range(Hkv):
+            bound = torch.where(ok, top[b, :, g][None], torch.zeros((), device="cuda")).amax(1)
+            assert (out[b, :, g * G:(g + 1) * G].float().abs().amax((1, 2)) <= bound * (1 + 2.0 ** -6)).all()
