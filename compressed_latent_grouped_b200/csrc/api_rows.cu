@@ -149,17 +149,17 @@ bool window_args(const Geo& g, const ccgqa_window* win, int B, int S, const ccgq
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255) == 0; }
 bool window_tc(const Geo& g, int max_group) { return g.dtype == CCGQA_BF16 && g.d >= 32 && g.G <= max_group; }
 // Statistics: a float per row, then a second one, or (tensor-core backward pass)
-// what rounding took from out, in bf16.
+// what rounding took from out, a byte per element.
 int64_t stats_floats(const Geo& g, int64_t B, int64_t S) {
   const int64_t rows = B * g.Hkv * stat_rows(g, S);
-  return rows + (window_tc(g, 64) ? B * S * g.Hq * g.d / 2 : rows);
+  return rows + (window_tc(g, 64) ? B * S * g.Hq * g.d / 4 : rows);
 }
 void set_stats(const Geo& g, float* stats, WindowArgs* a) {
   a->stats = stats;
   if (!stats) return;
   float* second = stats + static_cast<int64_t>(a->B) * g.Hkv * a->ld;
   if (window_tc(g, 64))
-    a->o_lo = reinterpret_cast<bf16*>(second);
+    a->o_lo = reinterpret_cast<int8_t*>(second);
   else
     a->inv_l = second;
 }

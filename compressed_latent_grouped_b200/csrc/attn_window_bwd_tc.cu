@@ -274,29 +274,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // -D = -rowsum(dO o), o with what its rounding dropped: D / 8 lanes read a row's 16-byte pieces, so that a warp's
       // loads cover whole lines (one thread per row took 17000 cycles at d = 128)
       constexpr int kLanes = D / 8, kStep = 32 / kLanes, kMine = kRows / kSoftWarps;
-      uint4 x4[kMine / kStep], y4[kMine / kStep], z4[kMine / kStep];
+      uint4 x4[kMine / kStep], y4[kMine / kStep];
+      uint2 z2[kMine / kStep];
 #pragma unroll
       for (int i = 0; i < kMine / kStep; ++i) {
         const int rr = (warp - 4) * kMine + i * kStep + lane / kLanes, uu = rr & 63;
         const int tt = t0 + (rr >> 6) * pos + uu / G, h = g * G + uu % G, e = lane % kLanes * 8;
-        x4[i] = y4[i] = z4[i] = make_uint4(0, 0, 0, 0);
+        x4[i] = y4[i] = make_uint4(0, 0, 0, 0);
+        z2[i] = make_uint2(0, 0);
         if (uu < used && tt < a.S) {
           x4[i] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.dout.ptr) + b * a.dout.batch + tt * a.dout.token + h * a.dout.head + e);
           y4[i] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.out.ptr) + b * a.out.batch + tt * a.out.token + h * a.out.head + e);
-          z4[i] = *reinterpret_cast<const uint4*>(a.o_lo + ((static_cast<int64_t>(b) * a.S + tt) * a.Hq + h) * D + e);
+          z2[i] = *reinterpret_cast<const uint2*>(a.o_lo + ((static_cast<int64_t>(b) * a.S + tt) * a.Hq + h) * D + e);
         }
       }
 #pragma unroll
       for (int i = 0; i < kMine / kStep; ++i) {
         const int rr = (warp - 4) * kMine + i * kStep + lane / kLanes, uu = rr & 63;
         const __nv_bfloat162* x2 = reinterpret_cast<const __nv_bfloat162*>(&x4[i]);
-        const __nv_bfloat162* y2 = reinterpret_cast<const __nv_bfloat162*>(&y4[i]);
-        const __nv_bfloat162* z2 = reinterpret_cast<const __nv_bfloat162*>(&z4[i]);
+        const uint32_t yw[4] = {y4[i].x, y4[i].y, y4[i].z, y4[i].w};
+        // the fp32 value's bits: bf16's, and the byte of what rounding took at bit 8
+        auto low = [&](int e) { return static_cast<int>((e < 4 ? z2[i].x : z2[i].y) << (24 - e % 4 * 8)) >> 24 << 8; };
         float acc = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 xf = __bfloat1622float2(x2[e]);
-          const float2 yf = fadd2(__bfloat1622float2(y2[e]), __bfloat1622float2(z2[e]));
+          const float2 yf = make_float2(__int_as_float(static_cast<int>(yw[e] << 16) + low(2 * e)),
+                                        __int_as_float(static_cast<int>(yw[e] & 0xffff0000u) + low(2 * e + 1)));
           acc = fmaf(xf.x, yf.x, acc);
           acc = fmaf(xf.y, yf.y, acc);
         }

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, FwdCfg<D, T>::kCtas)
         if (a.inv_l) a.inv_l[at] = inv_l;
       }
       bf16* dst = static_cast<bf16*>(a.out.ptr) + b * a.out.batch + t * a.out.token + (g * G + hl) * a.out.head;
-      bf16* lo = a.o_lo + ((static_cast<int64_t>(b) * a.S + t) * a.Hq + g * G + hl) * D;
+      int8_t* lo = a.o_lo + ((static_cast<int64_t>(b) * a.S + t) * a.Hq + g * G + hl) * D;
       uint8_t* stage = smem + C::kOffQ + x * C::kTileBytes + q4 * 2048;   // this tile's queries have been read
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -336,13 +336,23 @@ __global__ void __launch_bounds__(FwdCfg<D, T>::kThreads, FwdCfg<D, T>::kCtas)
         tmem_wait_ld();
         warp_store32(row_ok ? dst + c * 32 : nullptr, o, inv_l, stage, lane);
         if (a.o_lo != nullptr) {
-          // what the rounding dropped: the backward pass's D is that of the sum
+          // what the rounding dropped, for the backward pass's D: the distance of the
+          // fp32 value's bits from bf16's, rounded to the upper eight of its sixteen
+          uint32_t w[8];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float x = __uint_as_float(o[e]) * inv_l;
-            o[e] = __float_as_uint(x - __bfloat162float(__float2bfloat16_rn(x)));
+          for (int e = 0; e < 8; ++e) {
+            uint32_t pair[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float x0 = __uint_as_float(o[4 * e + 2 * y]) * inv_l, x1 = __uint_as_float(o[4 * e + 2 * y + 1]) * inv_l;
+              const uint32_t near = pack_bf16x2(x0, x1);
+              const int far0 = min(__float_as_int(x0) - static_cast<int>(near << 16) + 128, 32767);
+              const int far1 = min(__float_as_int(x1) - static_cast<int>(near & 0xffff0000u) + 128, 32767);
+              pair[y] = __byte_perm(far0, far1, 0x0051);
+            }
+            w[e] = __byte_perm(pair[0], pair[1], 0x5410);
           }
-          warp_store32(row_ok ? lo + c * 32 : nullptr, o, 1.f, stage, lane);
+          warp_store_bytes32(row_ok ? lo + c * 32 : nullptr, w, stage, lane);
         }
       }
     }

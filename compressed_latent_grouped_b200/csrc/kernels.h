@@ -308,7 +308,7 @@ struct WindowArgs {
   // formed from their one logarithm is off by its rounding.  dsum = -rowsum(dO o).
   float* stats;                 // forward: nullable
   float* inv_l;                 // null on the tensor-core path
-  bf16* o_lo;                   // tensor-core path: what rounding took from out, [B, S, Hq, d]
+  int8_t* o_lo;                 // tensor-core path: what rounding took from out, [B, S, Hq, d]: bits 8 to 15 of fp32
   float* dsum;
   int64_t ld;
   int pos;

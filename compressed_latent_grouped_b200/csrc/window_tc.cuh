@@ -78,6 +78,23 @@ __device__ __forceinline__ void warp_store32(bf16* dst, const uint32_t (&v)[32],
   __syncwarp();
 }
 
+// 32 bytes of each lane's row, likewise, two lanes a row.
+__device__ __forceinline__ void warp_store_bytes32(int8_t* dst, const uint32_t (&w)[8], uint8_t* stage, int lane) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    *reinterpret_cast<uint4*>(stage + lane * 32 + ((u ^ (lane >> 2)) & 1) * 16) =
+        make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = i * 16 + (lane >> 1), u = lane & 1;
+    const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 32 + ((u ^ (row >> 2)) & 1) * 16);
+    int8_t* p = reinterpret_cast<int8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
+    if (p != nullptr) *reinterpret_cast<uint4*>(p + u * 16) = x;
+  }
+  __syncwarp();
+}
+
 // Rows of `tiles` tiles of `rows` rows that the packed TMA box does not fill
 // (the group does not divide the tile): zeros, so that their products are
 // finite.  Called by all threads before the first product.
