@@ -5,7 +5,7 @@
 // Sums are fp32; P and dS are rounded to bf16 for the products; each gradient is
 // rounded once, at its store.
 //
-// Two kernels, each with one 128-row tile per CTA and blocks of 128 columns, so
+// Two kernels, each with tiles of 128 rows and blocks of 128 columns, so
 // that a product reads as many bytes of its A as of its B from shared memory (at
 // 128 x 64 or 128 x 32 the A operand, read again for every block, bounds it):
 //   dq pass   rows = packed queries (two groups of 64 rows, each 64 / G
@@ -26,6 +26,10 @@
 // below), two at d = 128, where dK and dV take half of TMEM.  The dq pass in halves
 // was slower at d = 128 (134 us against 129).
 //
+// The dq pass's CTAs take tile after tile, so that a tile's loads, its D and its
+// stores stand beside another's products (one tile per CTA: 132 us against 121 in the
+// first case below; window 2048, both passes: 367 us against 348).
+//
 // The dkv pass's work is cut evenly: the blocks of all key tiles, in order, are
 // shared out to one CTA per SM; a tile whose blocks end up in several CTAs leaves
 // fp32 partial sums that a third kernel adds in the order of the CTAs, so equal
@@ -34,8 +38,8 @@
 // more for the loads and stores around them: by blocks alone the CTAs at the short
 // tiles of a sequence's end ran 20 % longer than the rest.
 //
-// Measured: 32 / 8 heads of 128, 4096 tokens, window 1024: dq 132 us, dkv 134 us and
-// 10 us for its join, 680 and 900 TFLOP/s of the products they form.  8 / 2 heads of
+// Measured: 32 / 8 heads of 128, 4096 tokens, window 1024: dq 121 us, dkv 133 us and
+// 10 us for its join, 750 and 900 TFLOP/s of the products they form.  8 / 2 heads of
 // 64, 8192 tokens, window 4096: 117, 154 and 8 us, 660 and 670 TFLOP/s.  The bound is
 // the chain of each block, scores out of TMEM, exponentials and products, bf16 back
 // into TMEM: the tensor core is busy in 34 to 51 % of the cycles, the warps issue in
@@ -80,7 +84,7 @@ struct BwdCfg : RowTiles<D> {
   static constexpr int kSlots = D == 128 ? 2 : 3;             // dkv pass: half blocks, S | dP of 64 each
   static constexpr uint32_t kColV = kSlots * kRows, kColK = kColV + D;
   static_assert(kColK + D <= 512 && kColQ + D <= 512, "TMEM columns");
-  static_assert(kQSmem + 768 <= 227 * 1024 && kKSmem + 256 <= 227 * 1024, "shared memory, with the static part");
+  static_assert(kQSmem + 1152 <= 227 * 1024 && kKSmem + 256 <= 227 * 1024, "shared memory, with the static part");
 };
 
 // acc (+)= A B: A 128 x 128 bf16 in TMEM, 32 columns of it at the head of every 32
@@ -120,6 +124,67 @@ __device__ __forceinline__ void exp2_32(float (&p)[32]) {
 }
 
 // ================================================================ dq pass
+// Windows of more than so many blocks: two warps form D of the next tile, which takes
+// them about that long; with shorter ones all sixteen form each tile's own (window
+// 128 at d = 128, both passes: 129 us; ahead: 160).
+constexpr int kAhead = 7;
+
+// -D = -rowsum(dO o) of rows [r0, r0 + N) of a query tile into `out` and a.dsum, o
+// with what its rounding dropped, by one warp: D / 8 lanes read a row's 16-byte
+// pieces, so that a warp's loads cover whole lines (one thread per row took 17000
+// cycles at d = 128), of U rows a lane at once.
+template <int D, int N, int U>
+__device__ __forceinline__ void neg_row_sums(const WindowArgs& a, int b, int g, int64_t srow, int t0, int pos, int used, int r0,
+                                             float* out, int lane) {
+  constexpr int kLanes = D / 8, kStep = 32 / kLanes;
+  static_assert(N % (kStep * U) == 0, "rows of a warp");
+  const int G = a.G;
+#pragma unroll 1
+  for (int i0 = 0; i0 < N; i0 += kStep * U) {
+    uint4 x4[U], y4[U];
+    uint2 z2[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int rr = r0 + i0 + i * kStep + lane / kLanes, uu = rr & 63;
+      const int tt = t0 + (rr >> 6) * pos + uu / G, h = g * G + uu % G, e = lane % kLanes * 8;
+      x4[i] = y4[i] = make_uint4(0, 0, 0, 0);
+      z2[i] = make_uint2(0, 0);
+      if (uu < used && tt < a.S) {
+        x4[i] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.dout.ptr) + b * a.dout.batch + tt * a.dout.token + h * a.dout.head + e);
+        y4[i] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.out.ptr) + b * a.out.batch + tt * a.out.token + h * a.out.head + e);
+        z2[i] = *reinterpret_cast<const uint2*>(a.o_lo + ((static_cast<int64_t>(b) * a.S + tt) * a.Hq + h) * D + e);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int rr = r0 + i0 + i * kStep + lane / kLanes, uu = rr & 63;
+      const __nv_bfloat162* x2 = reinterpret_cast<const __nv_bfloat162*>(&x4[i]);
+      const uint32_t yw[4] = {y4[i].x, y4[i].y, y4[i].z, y4[i].w};
+      // the fp32 value's bits: bf16's, and the byte of what rounding took at bit 8
+      auto low = [&](int e) { return static_cast<int>((e < 4 ? z2[i].x : z2[i].y) << (24 - e % 4 * 8)) >> 24 << 8; };
+      float acc = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 xf = __bfloat1622float2(x2[e]);
+        const float2 yf = make_float2(__int_as_float(static_cast<int>(yw[e] << 16) + low(2 * e)),
+                                      __int_as_float(static_cast<int>(yw[e] & 0xffff0000u) + low(2 * e + 1)));
+        acc = fmaf(xf.x, yf.x, acc);
+        acc = fmaf(xf.y, yf.y, acc);
+      }
+#pragma unroll
+      for (int off = kLanes / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+      if (lane % kLanes == 0) {
+        out[rr] = -acc;
+        if (uu < used && t0 + (rr >> 6) * pos + uu / G < a.S) a.dsum[srow + rr] = -acc;
+      }
+    }
+  }
+}
+
+// A CTA works tiles one after another, the longest first, in an order that runs back
+// and forth over the CTAs so that their sums come out even.  While a tile is worked,
+// warps 2 and 3 form D of the next; its queries are loaded once the last scores have
+// read this one's, its dO once the gradients have been turned in that memory.
 template <int D>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     window_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
@@ -130,7 +195,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kQOffBar);
-  uint64_t* k_full = q_full + 1;
+  uint64_t* q_empty = q_full + 1;                // a tile's last scores issued
+  uint64_t* do_full = q_empty + 1;
+  uint64_t* tile_done = do_full + 1;             // sums and dO's memory read, one arrival per warp
+  uint64_t* k_full = tile_done + 1;
   uint64_t* k_empty = k_full + C::kKStages;
   uint64_t* v_full = k_empty + C::kKStages;
   uint64_t* v_empty = v_full + C::kVStages;
@@ -138,29 +206,46 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint64_t* s_read = s_full + 2;                 // [2], one arrival per warp
   uint64_t* dp_full = s_read + 2;                // [2]
   uint64_t* ds_full = dp_full + 2;               // [2], one arrival per warp
-  uint64_t* dq_done = ds_full + 2;
+  uint64_t* d_full = ds_full + 2;                // [2], by tile: D of its rows
+  uint64_t* d_read = d_full + 2;                 // [2], one arrival per warp
+  uint64_t* dq_done = d_read + 2;
   uint64_t* fin = dq_done + 1;
   uint64_t* drain = fin + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   __shared__ int abort_flag;
-  __shared__ float dpart[kRows];   // -D
+  __shared__ float dpart[2][kRows];   // -D
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  const int G = a.G, BH = a.B * a.Hkv;
-  const int tile = n_tiles - 1 - static_cast<int>(blockIdx.x) / BH;
-  const int bg = static_cast<int>(blockIdx.x) % BH;
-  const int b = bg / a.Hkv, g = bg % a.Hkv;
+  const int G = a.G;
+  const unsigned BH = a.B * a.Hkv;
   const int pos = 64 / G, used = pos * G;         // positions and rows of a group of 64 rows
-  const int t0 = tile * 2 * pos;
-  const int t_last = min(t0 + 2 * pos, a.S) - 1;
-  const int lo = max(0, t0 - a.window + 1);
-  const int sinks = min(a.sinks, lo);
-  const int n_sink = (sinks + kRows - 1) / kRows;
-  const int n = n_sink + (t_last - lo) / kRows + 1;
-  auto block = [&](int k) { return k < n_sink ? k * kRows : lo + (k - n_sink) * kRows; };
+  const bool ahead = a.window > kAhead * kRows;
+  // the CTA's i-th tile
+  struct Tile {
+    int tile, bg, b, g, t0, lo, sinks, n_sink, n;
+  };
+  auto get = [&](int i, Tile* s) {
+    const unsigned x = i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);   // below 2^31 + the grid
+    if (x >= static_cast<unsigned>(n_tiles) * BH) return false;
+    s->tile = n_tiles - 1 - static_cast<int>(x / BH);
+    s->bg = static_cast<int>(x % BH);
+    s->b = s->bg / a.Hkv;
+    s->g = s->bg % a.Hkv;
+    s->t0 = s->tile * 2 * pos;
+    const int t_last = min(s->t0 + 2 * pos, a.S) - 1;
+    s->lo = max(0, s->t0 - a.window + 1);
+    s->sinks = min(a.sinks, s->lo);
+    s->n_sink = (s->sinks + kRows - 1) / kRows;
+    s->n = s->n_sink + (t_last - s->lo) / kRows + 1;
+    return true;
+  };
+  auto block = [&](const Tile& s, int k) { return k < s.n_sink ? k * kRows : s.lo + (k - s.n_sink) * kRows; };
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(do_full, 1);
+    mbar_init(tile_done, kSoftWarps);
     for (int s = 0; s < C::kKStages; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
@@ -174,6 +259,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(&s_read[i], kSoftWarps);
       mbar_init(&dp_full[i], 1);
       mbar_init(&ds_full[i], kSoftWarps);
+      mbar_init(&d_full[i], 2);
+      mbar_init(&d_read[i], kSoftWarps);
     }
     mbar_init(dq_done, 1);
     mbar_init(fin, 1);
@@ -191,6 +278,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // k counts the CTA's blocks over all its tiles
   auto slot_s = [&](int k) { return tmem + static_cast<uint32_t>(2 * k % 3) * kRows; };
   auto slot_dp = [&](int k) { return tmem + static_cast<uint32_t>((2 * k + 1) % 3) * kRows; };
 
@@ -201,27 +289,39 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       prefetch_tensormap(&tmDO);
       prefetch_tensormap(&tmK);
       prefetch_tensormap(&tmV);
-      mbar_arrive_expect_tx(q_full, 4 * used * D * 2);
+      Tile s;
+      bool ok = true;
+      int k = 0;
+      for (int i = 0; ok && get(i, &s); ++i) {
+        auto load_rows = [&](uint32_t off, const CUtensorMap* tm, uint64_t* full) {
+          mbar_arrive_expect_tx(full, 2 * used * D * 2);
 #pragma unroll
-      for (int p = 0; p < C::kPanels; ++p)
+          for (int p = 0; p < C::kPanels; ++p)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t off = p * C::kPanel + j * 64 * C::kRowBytes;
-          tma_load_5d(smem + C::kQOffQ + off, &tmQ, q_full, p * C::kPanelCols, 0, g, t0 + j * pos, b);
-          tma_load_5d(smem + C::kQOffDO + off, &tmDO, q_full, p * C::kPanelCols, 0, g, t0 + j * pos, b);
+            for (int j = 0; j < 2; ++j)
+              tma_load_5d(smem + off + p * C::kPanel + j * 64 * C::kRowBytes, tm, full, p * C::kPanelCols, 0, s.g,
+                          s.t0 + j * pos, s.b);
+        };
+        if (!(ok = mbar_wait(q_empty, (i & 1) ^ 1, &abort_flag, a.dev_err))) break;
+        load_rows(C::kQOffQ, &tmQ, q_full);
+        for (int y = 0; y < s.n; ++y, ++k) {
+          const int ks = k % C::kKStages, vs = k % C::kVStages;
+          if (!(ok = mbar_wait(&k_empty[ks], ((k / C::kKStages) & 1) ^ 1, &abort_flag, a.dev_err))) break;
+          mbar_arrive_expect_tx(&k_full[ks], C::kTile);
+#pragma unroll
+          for (int p = 0; p < C::kPanels; ++p)
+            tma_load_4d(smem + C::kQOffK + ks * C::kTile + p * C::kPanel, &tmK, &k_full[ks], p * C::kPanelCols, block(s, y), s.g, s.b);
+          if (!(ok = mbar_wait(&v_empty[vs], ((k / C::kVStages) & 1) ^ 1, &abort_flag, a.dev_err))) break;
+          mbar_arrive_expect_tx(&v_full[vs], C::kTile);
+#pragma unroll
+          for (int p = 0; p < C::kPanels; ++p)
+            tma_load_4d(smem + C::kQOffV + vs * C::kTile + p * C::kPanel, &tmV, &v_full[vs], p * C::kPanelCols, block(s, y), s.g, s.b);
+          // dO waits for the tile before to end: after what can be loaded without
+          if (y == min(1, s.n - 1)) {
+            if (!(ok = mbar_wait(tile_done, (i & 1) ^ 1, &abort_flag, a.dev_err))) break;
+            load_rows(C::kQOffDO, &tmDO, do_full);
+          }
         }
-      for (int k = 0; k < n; ++k) {
-        const int ks = k % C::kKStages, vs = k % C::kVStages;
-        if (!mbar_wait(&k_empty[ks], ((k / C::kKStages) & 1) ^ 1, &abort_flag, a.dev_err)) break;
-        mbar_arrive_expect_tx(&k_full[ks], C::kTile);
-#pragma unroll
-        for (int p = 0; p < C::kPanels; ++p)
-          tma_load_4d(smem + C::kQOffK + ks * C::kTile + p * C::kPanel, &tmK, &k_full[ks], p * C::kPanelCols, block(k), g, b);
-        if (!mbar_wait(&v_empty[vs], ((k / C::kVStages) & 1) ^ 1, &abort_flag, a.dev_err)) break;
-        mbar_arrive_expect_tx(&v_full[vs], C::kTile);
-#pragma unroll
-        for (int p = 0; p < C::kPanels; ++p)
-          tma_load_4d(smem + C::kQOffV + vs * C::kTile + p * C::kPanel, &tmV, &v_full[vs], p * C::kPanelCols, block(k), g, b);
       }
     }
   } else if (warp == 1) {
@@ -229,16 +329,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (elect_one()) {
       const uint32_t idesc_s = make_idesc_bf16(128, kRows, false), idesc_o = make_idesc_bf16(128, D, true);
       const uint32_t q_base = smem_addr(smem + C::kQOffQ), do_base = smem_addr(smem + C::kQOffDO);
+      auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, &abort_flag, a.dev_err); };
       auto k_base = [&](int k) { return smem_addr(smem + C::kQOffK + k % C::kKStages * C::kTile); };
-      auto issue_s = [&](int k) {
-        if (!mbar_wait(&k_full[k % C::kKStages], (k / C::kKStages) & 1, &abort_flag, a.dev_err)) return false;
+      auto issue_s = [&](int k, bool last) {
+        if (!wait(&k_full[k % C::kKStages], k / C::kKStages)) return false;
         tc_fence_after();
         mma_rows_by_rows<D>(slot_s(k), q_base, C::kPanel, k_base(k), C::kPanel, idesc_s);
         mma_commit(&s_full[k & 1]);
+        if (last) mma_commit(q_empty);
         return true;
       };
       auto issue_dp = [&](int k) {
-        if (!mbar_wait(&v_full[k % C::kVStages], (k / C::kVStages) & 1, &abort_flag, a.dev_err)) return false;
+        if (!wait(&v_full[k % C::kVStages], k / C::kVStages)) return false;
         tc_fence_after();
         mma_rows_by_rows<D>(slot_dp(k), do_base, C::kPanel, smem_addr(smem + C::kQOffV + k % C::kVStages * C::kTile),
                             C::kPanel, idesc_s);
@@ -246,157 +348,161 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         mma_commit(&v_empty[k % C::kVStages]);
         return true;
       };
-      bool ok = mbar_wait(q_full, 0, &abort_flag, a.dev_err) && issue_s(0) && issue_dp(0) && (n < 2 || issue_s(1));
-      for (int k = 0; ok && k < n; ++k) {
-        // dP(k + 1) takes the slot of S(k) once it has been read, S(k + 2) that
-        // of dS(k) once dQ has read it
-        if (k + 1 < n && !(mbar_wait(&s_read[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err) && issue_dp(k + 1))) break;
-        if (!mbar_wait(&ds_full[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err)) break;
-        tc_fence_after();
-        mma_slot_by_rows<D>(tmem + C::kColQ, slot_dp(k), k_base(k), idesc_o, k == 0);
-        mma_commit(dq_done);
-        mma_commit(&k_empty[k % C::kKStages]);
-        if (k + 1 == n) mma_commit(fin);
-        if (k + 2 < n && !(mbar_wait(dq_done, k & 1, &abort_flag, a.dev_err) && issue_s(k + 2))) break;
-        if (k + 2 >= n && k + 1 < n && !mbar_wait(dq_done, k & 1, &abort_flag, a.dev_err)) break;
+      Tile s;
+      int k = 0;
+      bool ok = get(0, &s) && wait(q_full, 0) && issue_s(0, s.n == 1);
+      for (int i = 0; ok; ++i) {
+        // S of the tile's first block has been issued; its second's slot is that of
+        // the dS before, which dQ has read
+        const int end = k + s.n;
+        Tile next;
+        const bool more = get(i + 1, &next);
+        if (!(ok = (k == 0 || wait(dq_done, k - 1)) && (s.n < 2 || issue_s(k + 1, s.n == 2)) && wait(do_full, i) && issue_dp(k))) break;
+        for (const int first = k; ok && k < end; ++k) {
+          // the next tile's first S, one block early where there is one
+          const bool cross = more && k == (s.n > 1 ? end - 2 : first);
+          if (cross && s.n == 1 && !(ok = wait(q_full, i + 1) && issue_s(end, next.n == 1))) break;
+          // dP(k + 1) takes the slot of S(k) once it has been read, S(k + 2) that
+          // of dS(k) once dQ has read it
+          if (k + 1 < end && !(ok = wait(&s_read[k & 1], k >> 1) && issue_dp(k + 1))) break;
+          if (!(ok = wait(&ds_full[k & 1], k >> 1) && (k > first || i == 0 || wait(tile_done, i - 1)))) break;
+          tc_fence_after();
+          mma_slot_by_rows<D>(tmem + C::kColQ, slot_dp(k), k_base(k), idesc_o, k == first);
+          mma_commit(dq_done);
+          mma_commit(&k_empty[k % C::kKStages]);
+          if (k + 1 == end) {
+            mma_commit(fin);
+            continue;   // dq_done is waited for with the next tile's second block
+          }
+          if (!(ok = wait(dq_done, k))) break;
+          if (k + 2 < end)
+            ok = issue_s(k + 2, k + 3 == end);
+          else if (cross)
+            ok = wait(q_full, i + 1) && issue_s(end, next.n == 1);
+        }
+        if (!more) break;
+        s = next;
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ D of the next tile
+    Tile s;
+    for (int i = 1; ahead && get(i, &s); ++i) {
+      const int buf = i & 1;
+      // (the buffer's first tile, if it is the CTA's first, was formed by the warps below)
+      if (i > 1 && !mbar_wait(&d_read[buf], ((i >> 1) & 1) ^ 1, &abort_flag, a.dev_err)) break;
+      neg_row_sums<D, kRows / 2, 4>(a, s.b, s.g, s.bg * a.ld + static_cast<int64_t>(s.tile) * kRows, s.t0, pos, used,
+                                    (warp - 2) * (kRows / 2), dpart[buf], lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_full[buf]);
+    }
+  } else {
     // ------------------------------------------------------------ scores
     const int w = (warp - 4) >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane;                 // tile row == TMEM lane
-    const int u = r & 63, t = t0 + (r >> 6) * pos + u / G, hl = u % G;
-    const bool row_ok = u < used && t < a.S;
     const uint32_t trow = (static_cast<uint32_t>(q4 * 32) << 16) + w * 32;
-    const int64_t srow = bg * a.ld + static_cast<int64_t>(tile) * kRows + r;
-    const float nlse = row_ok ? a.stats[srow] : 0.f;   // -lse
-    {
-      // -D = -rowsum(dO o), o with what its rounding dropped: D / 8 lanes read a row's 16-byte pieces, so that a warp's
-      // loads cover whole lines (one thread per row took 17000 cycles at d = 128)
-      constexpr int kLanes = D / 8, kStep = 32 / kLanes, kMine = kRows / kSoftWarps;
-      uint4 x4[kMine / kStep], y4[kMine / kStep];
-      uint2 z2[kMine / kStep];
-#pragma unroll
-      for (int i = 0; i < kMine / kStep; ++i) {
-        const int rr = (warp - 4) * kMine + i * kStep + lane / kLanes, uu = rr & 63;
-        const int tt = t0 + (rr >> 6) * pos + uu / G, h = g * G + uu % G, e = lane % kLanes * 8;
-        x4[i] = y4[i] = make_uint4(0, 0, 0, 0);
-        z2[i] = make_uint2(0, 0);
-        if (uu < used && tt < a.S) {
-          x4[i] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.dout.ptr) + b * a.dout.batch + tt * a.dout.token + h * a.dout.head + e);
-          y4[i] = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.out.ptr) + b * a.out.batch + tt * a.out.token + h * a.out.head + e);
-          z2[i] = *reinterpret_cast<const uint2*>(a.o_lo + ((static_cast<int64_t>(b) * a.S + tt) * a.Hq + h) * D + e);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kMine / kStep; ++i) {
-        const int rr = (warp - 4) * kMine + i * kStep + lane / kLanes, uu = rr & 63;
-        const __nv_bfloat162* x2 = reinterpret_cast<const __nv_bfloat162*>(&x4[i]);
-        const uint32_t yw[4] = {y4[i].x, y4[i].y, y4[i].z, y4[i].w};
-        // the fp32 value's bits: bf16's, and the byte of what rounding took at bit 8
-        auto low = [&](int e) { return static_cast<int>((e < 4 ? z2[i].x : z2[i].y) << (24 - e % 4 * 8)) >> 24 << 8; };
-        float acc = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 xf = __bfloat1622float2(x2[e]);
-          const float2 yf = make_float2(__int_as_float(static_cast<int>(yw[e] << 16) + low(2 * e)),
-                                        __int_as_float(static_cast<int>(yw[e] & 0xffff0000u) + low(2 * e + 1)));
-          acc = fmaf(xf.x, yf.x, acc);
-          acc = fmaf(xf.y, yf.y, acc);
-        }
-#pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-        if (lane % kLanes == 0) {
-          dpart[rr] = -acc;
-          if (uu < used && t0 + (rr >> 6) * pos + uu / G < a.S)
-            a.dsum[bg * a.ld + static_cast<int64_t>(tile) * kRows + rr] = -acc;
-        }
-      }
-      named_barrier_sync(1, 32 * kSoftWarps);
-    }
-    const float nd = dpart[r];
     const float c = kLog2e * rsqrtf(static_cast<float>(D));
-    const float2 c2 = make_float2(c, c), nl2 = make_float2(nlse, nlse), nd2 = make_float2(nd, nd);
+    const int u = r & 63, hl = u % G;
+    Tile s;
     bool ok = true;
-    for (int k = 0; k < n; ++k) {
-      const int kb = block(k) + w * 32;
-      int begin = t - a.window + 1 - kb, end = min(t, a.S - 1) + 1 - kb, first = a.sinks - kb;
-      if (k < n_sink) {
-        begin = 32;
-        first = sinks - kb;
-      }
-      if (!row_ok) end = 0;
-      const bool whole = __all_sync(0xffffffffu, end >= 32 && (begin <= 0 || first >= 32));
-      const bool none = !whole && __all_sync(0xffffffffu, end <= 0 || (begin >= min(end, 32) && first <= 0));
-      if (!mbar_wait(&s_full[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err)) {
-        ok = false;
+    int k = 0;
+    for (int i = 0; ok && get(i, &s); ++i) {
+      const int t = s.t0 + (r >> 6) * pos + u / G;
+      const bool row_ok = u < used && t < a.S;
+      const int64_t srow = s.bg * a.ld + static_cast<int64_t>(s.tile) * kRows;
+      const float nlse = row_ok ? a.stats[srow + r] : 0.f;   // -lse
+      if (i == 0 || !ahead) {
+        constexpr int kMine = kRows / kSoftWarps, kStep = 256 / D;
+        neg_row_sums<D, kMine, kMine / kStep < 2 ? 1 : 2>(a, s.b, s.g, srow, s.t0, pos, used, (warp - 4) * kMine, dpart[i & 1], lane);
+        named_barrier_sync(1, 32 * kSoftWarps);
+      } else if (!mbar_wait(&d_full[i & 1], ((i - 1) >> 1) & 1, &abort_flag, a.dev_err)) {
         break;
       }
-      tc_fence_after();
-      float p[32];
-      if (!none) {
-        tmem_ld32(slot_s(k) + trow, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
-        tmem_wait_ld();
-      }
-      warp_arrive(&s_read[k & 1], lane);
-      // the first half of dP is on its way while the exponentials are formed
-      uint32_t dp0[16];
-      if (!mbar_wait(&dp_full[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      if (!none) {
-        tmem_ld16(slot_dp(k) + trow, dp0);
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 y = ffma2(make_float2(p[e], p[e + 1]), c2, nl2);
-          p[e] = y.x;
-          p[e + 1] = y.y;
+      const float nd = dpart[i & 1][r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&d_read[i & 1]);
+      const float2 c2 = make_float2(c, c), nl2 = make_float2(nlse, nlse), nd2 = make_float2(nd, nd);
+      for (int y = 0; y < s.n; ++y, ++k) {
+        const int kb = block(s, y) + w * 32;
+        int begin = t - a.window + 1 - kb, end = min(t, a.S - 1) + 1 - kb, first = a.sinks - kb;
+        if (y < s.n_sink) {
+          begin = 32;
+          first = s.sinks - kb;
         }
-        exp2_32(p);
-        if (!whole) {
-          const uint32_t seen = (below32(first) | ~below32(begin)) & below32(end);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) p[e] = (seen >> e) & 1 ? p[e] : 0.f;
+        if (!row_ok) end = 0;
+        const bool whole = __all_sync(0xffffffffu, end >= 32 && (begin <= 0 || first >= 32));
+        const bool none = !whole && __all_sync(0xffffffffu, end <= 0 || (begin >= min(end, 32) && first <= 0));
+        if (!mbar_wait(&s_full[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err)) {
+          ok = false;
+          break;
         }
-      }
-      uint32_t ds[16];
-      if (none) {
+        tc_fence_after();
+        float p[32];
+        if (!none) {
+          tmem_ld32(slot_s(k) + trow, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
+          tmem_wait_ld();
+        }
+        warp_arrive(&s_read[k & 1], lane);
+        // the first half of dP is on its way while the exponentials are formed
+        uint32_t dp0[16];
+        if (!mbar_wait(&dp_full[k & 1], (k >> 1) & 1, &abort_flag, a.dev_err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (!none) {
+          tmem_ld16(slot_dp(k) + trow, dp0);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ds[e] = 0;
-      } else {
-        uint32_t dp1[16];
-        tmem_wait_ld();
-        tmem_ld16(slot_dp(k) + trow + 16, dp1);
-        auto grads = [&](const uint32_t (&dp)[16], int at) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 y = fmul2(make_float2(p[at + 2 * e], p[at + 2 * e + 1]),
-                                   fadd2(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), nd2));
-            ds[at / 2 + e] = pack_bf16x2(y.x, y.y);
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = ffma2(make_float2(p[e], p[e + 1]), c2, nl2);
+            p[e] = x.x;
+            p[e + 1] = x.y;
           }
-        };
-        grads(dp0, 0);
-        tmem_wait_ld();
-        grads(dp1, 16);
+          exp2_32(p);
+          if (!whole) {
+            const uint32_t seen = (below32(first) | ~below32(begin)) & below32(end);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) p[e] = (seen >> e) & 1 ? p[e] : 0.f;
+          }
+        }
+        uint32_t ds[16];
+        if (none) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) ds[e] = 0;
+        } else {
+          uint32_t dp1[16];
+          tmem_wait_ld();
+          tmem_ld16(slot_dp(k) + trow + 16, dp1);
+          auto grads = [&](const uint32_t (&dp)[16], int at) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 x = fmul2(make_float2(p[at + 2 * e], p[at + 2 * e + 1]),
+                                     fadd2(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), nd2));
+              ds[at / 2 + e] = pack_bf16x2(x.x, x.y);
+            }
+          };
+          grads(dp0, 0);
+          tmem_wait_ld();
+          grads(dp1, 16);
+        }
+        tmem_st16(slot_dp(k) + trow, ds);
+        tmem_wait_st();
+        warp_arrive(&ds_full[k & 1], lane);
       }
-      tmem_st16(slot_dp(k) + trow, ds);
-      tmem_wait_st();
-      warp_arrive(&ds_full[k & 1], lane);
-    }
-    if (ok && mbar_wait(fin, 0, &abort_flag, a.dev_err)) {
-      tc_fence_after();
-      const float sc = rsqrtf(static_cast<float>(D));
-      bf16* dst = static_cast<bf16*>(a.dq.ptr) + b * a.dq.batch + t * a.dq.token + (g * G + hl) * a.dq.head;
+      if (!ok) break;
       // each warp 32 columns: at d < 128 the first D / 32 of a row's four
       if (w < D / 32) {
+        if (!mbar_wait(fin, i & 1, &abort_flag, a.dev_err)) break;
+        tc_fence_after();
+        bf16* dst = static_cast<bf16*>(a.dq.ptr) + s.b * a.dq.batch + t * a.dq.token + (s.g * G + hl) * a.dq.head;
         uint32_t v[32];
         tmem_ld32(tmem + C::kColQ + trow, v);
         tmem_wait_ld();
-        // Q and dO have been read: 2 KB of them per warp
-        warp_store32(row_ok ? dst + w * 32 : nullptr, v, sc, smem + C::kQOffQ + (warp - 4) * 2048, lane);
+        // dO has been read: 2 KB of it per warp
+        warp_store32(row_ok ? dst + w * 32 : nullptr, v, rsqrtf(static_cast<float>(D)), smem + C::kQOffDO + (warp - 4) * 2048, lane);
+        fence_proxy_async_smem();
       }
+      warp_arrive(tile_done, lane);
     }
   }
 
@@ -917,7 +1023,7 @@ cudaError_t launch_bwd(const WindowArgs& a, cudaStream_t stream) {
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_dq_tc_kernel<D>), static_cast<int>(C::kQSmem));
   if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(window_dkv_tc_kernel<D>), static_cast<int>(C::kKSmem));
   if (e != cudaSuccess) return e;
-  e = launch_pdl(window_dq_tc_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(kBwdThreads), C::kQSmem, stream, tmQ,
+  e = launch_pdl(window_dq_tc_kernel<D>, dim3(static_cast<unsigned>(std::min<int64_t>(grid, sm_count()))), dim3(kBwdThreads), C::kQSmem, stream, tmQ,
                  tmDO, tmK, tmV, a, static_cast<int>(n_tiles));
   if (e != cudaSuccess) return e;
   count_launches(1);

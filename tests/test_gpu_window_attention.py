@@ -385,3 +385,30 @@ def test_tiles_left_over(Bn, S, Hq, Hkv, d, window, sinks):
         for g in range(Hkv):
             bound = torch.where(ok, top[b, :, g][None], torch.zeros((), device="cuda")).amax(1)
             assert (out[b, :, g * G:(g + 1) * G].float().abs().amax((1, 2)) <= bound * (1 + 2.0 ** -6)).all()
+
+
+@pytest.mark.parametrize("Bn,S,Hq,Hkv,d,window,sinks", [
+    (2, 2000, 32, 8, 64, 0, 0),          # seven query tiles per CTA, of every length
+    (1, 3000, 24, 8, 128, 1000, 37),     # groups of three: rows left over
+    (3, 1500, 32, 8, 32, 900, 0),
+    (2, 1700, 32, 8, 64, 200, 300),      # short windows: D formed tile by tile
+    (4, 640, 64, 16, 128, 1, 0),         # tiles of one block
+])
+def test_gradients_of_many_query_tiles(Bn, S, Hq, Hkv, d, window, sinks):
+    """CTAs that take several query tiles one after another; some heads against float64."""
+    cfg = config(Hq, Hkv, d)
+    q, k, v, do = inputs(Bn, S, Hq, Hkv, d, "bf16", seed=5)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(window=window, sinks=sinks, dev_err=err)
+    out, stats = window_attention(cfg, q, k, v, with_stats=True, **kw)
+    got = window_attention_backward(cfg, q, k, v, out, stats, do, **kw)
+    again = window_attention_backward(cfg, q, k, v, out, stats, do, **kw)
+    assert int(err) == 0
+    for x, y in zip(got, again):
+        assert torch.equal(x, y), "equal calls, other bits"
+    G = Hq // Hkv
+    for g in {0, Hkv // 2, Hkv - 1}:
+        hs, kv = slice(g * G, g * G + G), slice(g, g + 1)
+        ref, tol = reference(q[:, :, hs], k[:, :, kv], v[:, :, kv], window, sinks, do[:, :, hs])
+        for m, x, sl in zip(("dq", "dk", "dv"), got, (hs, kv, kv)):
+            close(x[:, :, sl], ref[m], tol[m], f"{m}, kv head {g}")
