@@ -27,7 +27,7 @@
 // was slower at d = 128 (134 us against 129).
 //
 // The dq pass's CTAs take tile after tile, so that a tile's loads, its D and its
-// stores stand beside another's products (one tile per CTA: 132 us against 121 in the
+// stores stand beside another's products (one tile per CTA: 132 us against 118 in the
 // first case below; window 2048, both passes: 367 us against 348).
 //
 // The dkv pass's work is cut evenly: the blocks of all key tiles, in order, are
@@ -38,11 +38,11 @@
 // more for the loads and stores around them: by blocks alone the CTAs at the short
 // tiles of a sequence's end ran 20 % longer than the rest.
 //
-// Measured: 32 / 8 heads of 128, 4096 tokens, window 1024: dq 121 us, dkv 133 us and
-// 10 us for its join, 750 and 900 TFLOP/s of the products they form.  8 / 2 heads of
-// 64, 8192 tokens, window 4096: 117, 154 and 8 us, 660 and 670 TFLOP/s.  The bound is
+// Measured: 32 / 8 heads of 128, 4096 tokens, window 1024: dq 118 us, dkv 133 us and
+// 10 us for its join, 760 and 900 TFLOP/s of the products they form.  8 / 2 heads of
+// 64, 8192 tokens, window 4096: 115, 155 and 8 us, 670 and 670 TFLOP/s.  The bound is
 // the chain of each block, scores out of TMEM, exponentials and products, bf16 back
-// into TMEM: the tensor core is busy in 34 to 51 % of the cycles, the warps issue in
+// into TMEM: the tensor core is busy in 34 to 52 % of the cycles, the warps issue in
 // 38 to 49 %, memory is idle.  Both passes form the scores anew, 7 products where
 // 5 would do, because one pass over both needs atomic sums of dq.
 //
